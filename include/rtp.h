@@ -315,6 +315,158 @@ RTP_API rtp_status rtp_dense_attn(const rtp_shape* shape, rtp_view q, rtp_view k
                           float softmax_scale, rtp_view o, float* lse, void* ws,
                           size_t ws_bytes, rtp_stream_t stream);
 
+/*
+ * Paged KV cache: requests of different lengths share one pool of pages.
+ *
+ * A page holds page_size (16, 32, 64, 128 or 256) consecutive positions of one
+ * request, for every kv head.  Row b of the block table names the pages of
+ * request b in order: position x lies in row x % page_size of page
+ * block_table[b * table_stride + x / page_size].  A page belongs to one request.
+ * K and V pages are bf16, or e4m3 with one fp32 scale per kv head (value =
+ * scale * stored; a null scale array means 1), in any order of rows and heads:
+ * strides are in elements, all multiples of 16 bytes.  Head dimension 128, at
+ * most 16 query heads per kv head, kv_role as everywhere (1 = retrieval).
+ *
+ * Lengths, tables and lists are DEVICE arrays: no call needs them on the host,
+ * so a step can be captured once in a CUDA graph and replayed while the
+ * requests grow.  Entries that cannot be meant (a negative length, a length
+ * beyond the table, a page outside the pool) are never followed: such keys count
+ * as absent, such rows are not written.  A table covers at most 2^30 positions.
+ * The workspaces of these calls need no initialisation and carry nothing from
+ * one call to the next; concurrent calls must not share one.
+ */
+typedef enum rtp_kv_type { RTP_KV_BF16 = 0, RTP_KV_E4M3 = 1 } rtp_kv_type;
+
+typedef struct rtp_pages {
+    void* ptr;           /* device pointer to page 0, row 0, head 0 */
+    int64_t stride_page; /* elements between pages */
+    int64_t stride_row;  /* elements between positions of a page */
+    int64_t stride_head; /* elements between kv heads; a head's 128 are contiguous */
+    int32_t n_pages;
+    int32_t page_size;
+    int32_t type;        /* rtp_kv_type */
+} rtp_pages;
+
+typedef enum rtp_paged_op {
+    RTP_PAGED_PLAN = 0,
+    RTP_PAGED_SELECT = 1,
+    RTP_PAGED_ATTN = 2
+} rtp_paged_op;
+
+/* Bytes of workspace a paged call needs (always >= 256); H, Hkv, kv_role and
+ * table_width (pages per block-table row) as in that call, ignored for
+ * RTP_PAGED_PLAN. */
+RTP_API size_t rtp_paged_workspace_size(rtp_paged_op op, int32_t B, int32_t H, int32_t Hkv,
+                                        const uint8_t* kv_role, int32_t table_width);
+
+/*
+ * Pages, slots and spans of a step.  Request b has seq_lens[b] tokens (none, and
+ * its pages back on the free stack first, where release[b] != 0; release may be
+ * null) and gets n_new[b] more.  The batch of new tokens is packed in request
+ * order (row_tokens = 0), or padded: request b's tokens start at b * row_tokens
+ * and are at most row_tokens.  Free pages are a stack: free_pages[0 ..
+ * *free_count), taken from the end, requests in order.
+ *  - A request is refused, whole, if its tokens do not fit its table row, the
+ *    batch (max_tokens, row_tokens) or the free pages; requests behind one that the
+ *    pages did not suffice for are admitted only if they need none.  A
+ *    refused request keeps its length (0 after a release); its tokens get slot -1.
+ *  - block_table: the new pages' entries are written, nothing else.
+ *  - seq_lens_out[B], admitted[B] (1 or 0), cu_new[B + 1] (first token of each
+ *    request in the batch, refused ones counted, saturating), *free_count_out.
+ *    seq_lens_out may be seq_lens, free_count_out may be free_count.
+ *  - slot_map[max_tokens]: page * page_size + row of each token, -1 elsewhere.
+ *  - spans[max_spans][4]: {page, rows, fresh, token} for every page a request's
+ *    new tokens touch: rows it holds afterwards, rows it held before, and the
+ *    index in the batch of the token in its first new row; page -1 behind the last.
+ *    min(max_tokens, max_tokens / page_size + 2 B) spans always suffice; further
+ *    ones are dropped.  16-byte aligned.
+ * free_cap: entries of free_pages (pages released beyond it are dropped).
+ * Workspace: rtp_paged_workspace_size(RTP_PAGED_PLAN, B, ...).
+ */
+RTP_API rtp_status rtp_paged_plan(int32_t B, int32_t page_size, int32_t row_tokens,
+                                  const int32_t* seq_lens, const int32_t* n_new,
+                                  const uint8_t* release,
+                                  int32_t* block_table, int64_t table_stride, int32_t table_width,
+                                  int32_t* free_pages, int32_t free_cap, const int32_t* free_count,
+                                  int32_t max_tokens, int32_t max_spans, int32_t* seq_lens_out,
+                                  int32_t* cu_new, int32_t* slot_map, int32_t* spans,
+                                  int32_t* free_count_out, int32_t* admitted, void* ws,
+                                  size_t ws_bytes, rtp_stream_t stream);
+
+/*
+ * Writes T tokens' K and V rows (bf16, row t at k + t * k_stride elements, Hkv
+ * heads of 128 contiguous, 16-byte aligned) to slots slot_map[t]; a slot outside
+ * the pool (-1) skips its token.  Two tokens must not name one slot.  8-bit pages
+ * get e4m3(x / scale[head]): an fp32 division, one rounding to nearest even,
+ * saturating at 448.  No workspace.
+ */
+RTP_API rtp_status rtp_paged_kv_write(int32_t T, int32_t Hkv, const void* k, int64_t k_stride,
+                                      const void* v, int64_t v_stride, const int32_t* slot_map,
+                                      rtp_pages k_pages, rtp_pages v_pages, const float* k_scale,
+                                      const float* v_scale, rtp_stream_t stream);
+
+/*
+ * The same rows by the spans of rtp_paged_plan, and the bounds of every page they
+ * touch, in one pass.  bounds [n_pages][retrieval kv heads][2][128] int8 (16-byte
+ * aligned) and bound_scale [n_pages][retrieval kv heads] fp32, per page over all
+ * rows that it then holds, stored values k (8-bit rows without their scale):
+ *   lo_d = min k_d, hi_d = max k_d, s = max_d max(|lo_d|, |hi_d|) * (1/127)  (fp32),
+ *   bounds[0][d] = max(-127, floor(lo_d / s)), bounds[1][d] = min(127, ceil(hi_d / s)).
+ * All zero with s = 0 where every value is zero, with s = inf where one is not
+ * finite.  Two spans must not name one page.  No workspace.
+ */
+RTP_API rtp_status rtp_paged_kv_append(int32_t T, int32_t Hkv, const uint8_t* kv_role,
+                                       const void* k, int64_t k_stride, const void* v,
+                                       int64_t v_stride, const int32_t* spans, int32_t n_spans,
+                                       rtp_pages k_pages, rtp_pages v_pages, const float* k_scale,
+                                       const float* v_scale, int8_t* bounds, float* bound_scale,
+                                       rtp_stream_t stream);
+
+/*
+ * The pages one new token per request attends to: for every request and
+ * retrieval kv head (G query heads, q row of request b at q + b * q_stride
+ * elements, H heads of 128), the n_sel best pages of 0 .. ceil(len / page_size),
+ *   a_h = max_d |q_hd|, sq_h = a_h * (1/127), q8_hd = rint(q_hd / sq_h)  (fp32),
+ *   I_h = sum_d max(q8_hd * bounds[0][d], q8_hd * bounds[1][d])      (whole numbers),
+ *   score = max_h float(I_h) * (sq_h * bound_scale),
+ * ties to the lower page; the first n_first and the last n_recent pages always
+ * (n_first + n_recent <= n_sel).  A page with bound_scale = inf scores inf; a
+ * head of q that is zero or not finite scores 0 everywhere.  seq_lens counts the
+ * new token.
+ * sel [B][retrieval kv heads][n_sel]: block-table columns, ascending, -1 behind
+ * the last; sel_count [B][retrieval kv heads].
+ * Workspace: rtp_paged_workspace_size(RTP_PAGED_SELECT, ...).
+ */
+RTP_API rtp_status rtp_paged_block_select(
+    int32_t B, int32_t H, int32_t Hkv, const uint8_t* kv_role, const void* q, int64_t q_stride,
+    const int8_t* bounds, const float* bound_scale, int32_t n_pages, int32_t page_size,
+    const int32_t* block_table, int64_t table_stride, int32_t table_width,
+    const int32_t* seq_lens, int32_t n_sel, int32_t n_first, int32_t n_recent, int32_t* sel,
+    int32_t* sel_count, void* ws, size_t ws_bytes, rtp_stream_t stream);
+
+/*
+ * Attention of one new token per request (its K/V rows already in the pages,
+ * seq_lens counts it), every head in one call:
+ *  - retrieval kv heads: keys 0 .. len - 1; with sel (rtp_paged_block_select's
+ *    lists, distinct columns) the keys of the listed pages;
+ *  - local kv heads: keys j < len with j < n_sink or j >= len - window
+ *    [FASB §Local Head Attention Pattern]; window >= 1, n_sink >= 0 (not read
+ *    without local heads).
+ * q, o: row of request b at q + b * q_stride elements, H heads of 128 bf16.  lse
+ * (nullable): [B][H] fp32, natural log of the softmax denominator including the
+ * scale.  A request without keys gets o = 0, lse = -inf; a key whose score is
+ * -inf counts as absent.  The result does not depend on the other requests beyond
+ * fp32 rounding (they share the split) and is the same on every run.
+ * Workspace: rtp_paged_workspace_size(RTP_PAGED_ATTN, ...).
+ */
+RTP_API rtp_status rtp_paged_attn_decode(
+    int32_t B, int32_t H, int32_t Hkv, const uint8_t* kv_role, int32_t window, int32_t n_sink,
+    const void* q, int64_t q_stride, rtp_pages k_pages, rtp_pages v_pages, const float* k_scale,
+    const float* v_scale, const int32_t* block_table, int64_t table_stride, int32_t table_width,
+    const int32_t* seq_lens, const int32_t* sel, const int32_t* sel_count, int32_t n_sel,
+    float softmax_scale, void* o, int64_t o_stride, float* lse, void* ws, size_t ws_bytes,
+    rtp_stream_t stream);
+
 /* Human-readable name of a status code (static storage). */
 RTP_API const char* rtp_status_string(rtp_status status);
 

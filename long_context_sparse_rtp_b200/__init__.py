@@ -2,8 +2,8 @@
 
 The product is the C-ABI library ``librtp.so`` (``include/rtp.h``); this package
 holds its CUDA sources (``csrc/``), the build step (``build.py``), a thin ctypes
-binding with the same entry-point names (``rtp.py``), a layer-level convenience
-wrapper (``layer.py``) and the seeded synthetic-input generator (``synth.py``).
+binding with the same entry-point names (``rtp.py``, ``paged.py``), a layer-level
+convenience wrapper (``layer.py``) and the seeded synthetic-input generator (``synth.py``).
 Importing the package does not load the library; the first call does, and fails
 loudly if it is not built.
 """
@@ -25,4 +25,17 @@ from .rtp import (  # noqa: F401
     rtp_version,
     rtp_workspace_size,
 )
-from .layer import DecodeGraph, rtp_layer_decode, rtp_layer_prefill  # noqa: F401
+from .paged import (  # noqa: F401
+    rtp_paged_attn_decode,
+    rtp_paged_block_select,
+    rtp_paged_kv_append,
+    rtp_paged_kv_write,
+    rtp_paged_plan,
+)
+from .layer import (  # noqa: F401
+    DecodeGraph,
+    PagedCache,
+    rtp_layer_decode,
+    rtp_layer_decode_paged,
+    rtp_layer_prefill,
+)

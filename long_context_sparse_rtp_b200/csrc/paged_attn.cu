@@ -1,0 +1,668 @@
+// paged_attn.cu -- attention of one new token per request over a paged KV cache
+// (rtp_paged_attn_decode).
+//
+//   o_h = sum_j softmax_j(scale * q_h . k_j) v_j
+// over the request's keys: every key (retrieval heads), the keys of the listed
+// pages (retrieval heads with a selection), or sinks and window (local heads).
+// One pass with a running maximum and sum; requests of all lengths share the
+// GPU evenly: the tiles of 64 keys of every (request, kv head) stand in one
+// line, and each CTA takes an equal run of them.  A (request, kv head) that one
+// CTA covers is written by it; one that several cover leaves partial results
+// (m, l, o), which a second kernel joins in CTA order.
+//
+// Within a tile each of the 4 warps has a group of 16 keys, which lies in one
+// page, and its own ring of shared-memory stages filled by cp.async: no barrier
+// inside a run of tiles.  Tensor-core products have the G query heads as their
+// (up to 16) rows.  Bound by HBM: 4 G flops a byte of bf16 K/V.
+//
+// Rounding: scores, maxima, sums and outputs in fp32; P is rounded once to the
+// 16-bit type of the P V product (bf16 beside bf16 rows; fp16 beside 8-bit ones,
+// whose values fp16 holds exactly), its row sums are taken before that rounding.
+// Beside 8-bit rows q is held in fp16, shifted by a power of two to a maximum in
+// [2^14, 2^15): exact but for elements under 2^-28 of the head's largest.
+#include "paged.cuh"
+
+namespace rtp {
+namespace {
+
+struct PagedAttnParams {
+  const uint16_t* q; int64_t q_sb;
+  uint16_t* o; int64_t o_sb;
+  float* lse;                     // [B][H] or null
+  PageAddr kp, vp;
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* table; int64_t table_stride;
+  const int32_t* seq_lens;
+  const int32_t* sel;             // [B][n_rkv][n_sel]
+  const int32_t* sel_count;       // [B][n_rkv]
+  float* part;                    // [CTAs][2][G][kPartRow]
+  int64_t* meta;                  // tiles per CTA; then each row's first tile
+  float scale_log2;
+  int32_t B, G, Hkv, n_rkv, H, n_pages, width, ps_shift, window, n_sink, n_sel;
+  int16_t head[kMaxHeads];
+};
+
+constexpr int kAttnThreads = 128;
+constexpr int kAttnWarps = kAttnThreads / 32;
+
+// Tokens of request b, as far as its table can hold them.
+__device__ __forceinline__ int paged_len(const PagedAttnParams& p, int b) {
+  return (int)min((int64_t)max(0, p.seq_lens[b]), (int64_t)p.width << p.ps_shift);
+}
+
+// Groups of 16 keys that hold the sinks and the window of a local head: sink
+// groups [0, n0), then groups from w0 on.
+struct LocalRange {
+  int n0, w0, total, win_lo;
+};
+__device__ __forceinline__ LocalRange local_range(const PagedAttnParams& p, int len) {
+  LocalRange r;
+  const int ng = (len + kGroup - 1) / kGroup;
+  r.win_lo = max(0, len - p.window);
+  r.n0 = (min(p.n_sink, len) + kGroup - 1) / kGroup;
+  r.w0 = max(r.n0, r.win_lo / kGroup);
+  r.total = r.n0 + max(0, ng - r.w0);
+  return r;
+}
+
+template <bool SEL>
+__device__ __forceinline__ int row_groups(const PagedAttnParams& p, int b, int i, int len) {
+  if (i >= p.n_rkv) return local_range(p, len).total;
+  if (SEL)
+    return len > 0 ? max(0, min(p.sel_count[b * p.n_rkv + i], p.n_sel)) << (p.ps_shift - 4) : 0;
+  return (len + kGroup - 1) / kGroup;
+}
+__device__ __forceinline__ int tiles_of(int groups) { return (groups + kAttnWarps - 1) / kAttnWarps; }
+
+template <bool SEL>
+__device__ __forceinline__ int64_t request_tiles(const PagedAttnParams& p, int b) {
+  const int len = paged_len(p, b);
+  int64_t n = 0;
+  if (p.Hkv > p.n_rkv) n = (int64_t)(p.Hkv - p.n_rkv) * tiles_of(row_groups<SEL>(p, b, p.n_rkv, len));
+  if (SEL) {
+    for (int i = 0; i < p.n_rkv; ++i) n += tiles_of(row_groups<SEL>(p, b, i, len));
+  } else if (p.n_rkv > 0) {
+    n += (int64_t)p.n_rkv * tiles_of(row_groups<SEL>(p, b, 0, len));
+  }
+  return n;
+}
+
+__device__ __forceinline__ void mma16816_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                             uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+constexpr float kPShift = 14.f;  // P is held as 2^14 p in fp16: subnormal only under 2^-28
+
+// One warp's stages.  K rows: bf16 swizzled by row & 7 (ldmatrix), 8-bit by
+// (row & 1) << 2; V rows: bf16 by row & 7, 8-bit by ((row >> 1) & 3) << 1: each
+// makes the eight 16-byte reads of a quarter warp fall on different banks.
+template <bool E4M3>
+struct WarpStages {
+  static constexpr int kRow = E4M3 ? kD : 2 * kD;          // bytes
+  static constexpr int kStages = E4M3 ? 6 : 3;
+  uint8_t k[kStages][kGroup][kRow];
+  uint8_t v[kStages][kGroup][kRow];
+};
+
+template <bool E4M3>
+struct AttnSmem {
+  WarpStages<E4M3> w[kAttnWarps];  // a finished run's partial outputs reuse each warp's stages
+  uint32_t mask[kAttnWarps][8];    // per stage: bit r = key r of the group counts
+  float wm[kAttnWarps][16], wl[kAttnWarps][16];
+  int64_t sums[kAttnWarps], first;
+  int req;
+};
+static_assert(sizeof(WarpStages<true>) >= 16 * kD * 4, "partials fit a warp's stages");
+static_assert(sizeof(WarpStages<false>) >= 16 * kD * 4, "partials fit a warp's stages");
+
+// Where a run's results go: o and lse, or a partial.
+__device__ __forceinline__ void store_final(const PagedAttnParams& p, int b, int g, int r, int d,
+                                            float m, float l, float o) {
+  const int h = g * p.G + r;
+  const float vs = p.v_scale ? p.v_scale[g] : 1.f;
+  const float x = l > 0.f || l != l ? o / l * vs : 0.f;
+  p.o[b * p.o_sb + (int64_t)h * kD + d] = __bfloat16_as_ushort(__float2bfloat16_rn(x));
+  if (d == 0 && p.lse != nullptr)
+    p.lse[(int64_t)b * p.H + h] = l > 0.f || l != l ? (m + log2f(l)) * kLn2 : -INFINITY;
+}
+
+template <bool E4M3, bool SEL>
+__global__ void __launch_bounds__(kAttnThreads) paged_attn_kernel(const PagedAttnParams p) {
+  griddep_wait();
+  extern __shared__ __align__(128) unsigned char smem_raw[];
+  AttnSmem<E4M3>& sm = *reinterpret_cast<AttnSmem<E4M3>*>(smem_raw);
+  constexpr int kRow = WarpStages<E4M3>::kRow, kStages = WarpStages<E4M3>::kStages;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, t = lane & 3;
+
+  // ---- this CTA's run of tiles
+  auto scan = [&](int64_t v, int64_t& all) {  // exclusive over the CTA
+    int64_t x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) sm.sums[warp] = x;
+    __syncthreads();
+    int64_t before = 0;
+    all = 0;
+#pragma unroll
+    for (int w = 0; w < kAttnWarps; ++w) {
+      if (w < warp) before += sm.sums[w];
+      all += sm.sums[w];
+    }
+    return before + x - v;
+  };
+  int64_t W = 0;
+  for (int b0 = 0; b0 < p.B; b0 += kAttnThreads) {
+    int64_t all;
+    scan(b0 + tid < p.B ? request_tiles<SEL>(p, b0 + tid) : 0, all);
+    W += all;
+  }
+  const int64_t chunk = max((int64_t)1, (W + gridDim.x - 1) / gridDim.x);
+  if (blockIdx.x == 0 && tid == 0) p.meta[0] = chunk;
+  int64_t pos = (int64_t)blockIdx.x * chunk;
+  const int64_t end = min(W, pos + chunk);
+  if (pos >= end) return;
+  for (int64_t b0 = 0, run = 0; b0 < p.B && run <= pos; b0 += kAttnThreads) {
+    int64_t all;
+    const int b = (int)b0 + tid;
+    const int64_t n = b < p.B ? request_tiles<SEL>(p, b) : 0;
+    const int64_t at = run + scan(n, all);
+    if (at <= pos && pos < at + n) {
+      sm.req = b;
+      sm.first = at;
+    }
+    run += all;
+  }
+  __syncthreads();
+  int b = sm.req, i = 0;
+  int len = paged_len(p, b);
+  int64_t row0 = sm.first;  // first tile of row (b, i)
+  const int64_t start = pos;
+
+  uint8_t* const kst = &sm.w[warp].k[0][0][0];
+  uint8_t* const vst = &sm.w[warp].v[0][0][0];
+  constexpr int kStageBytes = kGroup * kRow;
+
+  for (;;) {
+    // ---- the row that holds tile `pos`
+    int groups = row_groups<SEL>(p, b, i, len);
+    while (row0 + tiles_of(groups) <= pos) {
+      row0 += tiles_of(groups);
+      if (++i == p.Hkv) {
+        i = 0;
+        len = paged_len(p, ++b);
+      }
+      groups = row_groups<SEL>(p, b, i, len);
+    }
+    const int head = p.head[i];
+    const int t0 = (int)(pos - row0), tiles = tiles_of(groups);
+    const int t1 = (int)min((int64_t)tiles, t0 + (end - pos));
+    const LocalRange lr = local_range(p, len);
+    const bool local = i >= p.n_rkv;
+    if (t0 == 0 && tid == 0) p.meta[1 + (int64_t)b * p.Hkv + i] = pos;
+
+    // ---- query rows g and g + 8 as product operands
+    uint32_t qa[8][4];
+    float ms[2] = {p.scale_log2, p.scale_log2};  // score multiplier of each row
+    {
+      const uint16_t* qb = p.q + b * p.q_sb + (int64_t)head * p.G * kD;
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = g + 8 * (e & 1);
+          // 8-bit rows are read 16 bytes a thread: product kk of 16 bytes j takes
+          // dimensions 64 j + 16 t + 4 (kk % 4) + {0, 1 | 2, 3}
+          const int d = E4M3 ? 64 * (kk >> 2) + 16 * t + 4 * (kk & 3) + 2 * (e >> 1)
+                             : 16 * kk + 8 * (e >> 1) + 2 * t;
+          qa[kk][e] = r < p.G ? *reinterpret_cast<const uint32_t*>(qb + r * kD + d) : 0u;
+        }
+      if (E4M3) {
+        const float ks = p.k_scale ? p.k_scale[head] : 1.f;
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          float a = 0.f;
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+#pragma unroll
+            for (int e = hh; e < 4; e += 2)
+              a = fmaxf(a, fmaxf(fabsf(bf16_lo(qa[kk][e])), fabsf(bf16_hi(qa[kk][e]))));
+          a = quad_max(a);
+          int ex = (int)((__float_as_uint(a) >> 23) & 0xFF) - 127;
+          ex = a > 0.f ? max(-100, min(ex, 127)) : 14;
+          const float up = __uint_as_float((uint32_t)(14 - ex + 127) << 23);
+          ms[hh] *= ks * __uint_as_float((uint32_t)(ex - 14 + 127) << 23);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+#pragma unroll
+            for (int e = hh; e < 4; e += 2)
+              qa[kk][e] = pack_f16x2(bf16_lo(qa[kk][e]) * up, bf16_hi(qa[kk][e]) * up);
+        }
+      }
+    }
+
+    float oacc[16][4];
+#pragma unroll
+    for (int d = 0; d < 16; ++d)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) oacc[d][e] = 0.f;
+    float mrow[2] = {-INFINITY, -INFINITY};
+    float lrow[2] = {0.f, 0.f};
+
+    // ---- this warp's groups: tile tt of the run is group 4 (t0 + tt) + warp
+    const int n_run = t1 - t0;
+    const int32_t* tab = p.table + (int64_t)b * p.table_stride;
+    const int32_t* sl = SEL ? p.sel + ((int64_t)b * p.n_rkv + (local ? 0 : i)) * p.n_sel : nullptr;
+    // first key and physical page of a tile's group; page -1 where there is none
+    auto locate = [&](int tt, int& key0, int& page) {
+      const int gi = kAttnWarps * (t0 + tt) + warp;
+      key0 = 0;
+      page = -1;
+      if (tt >= n_run || gi >= groups) return;
+      if (local) {
+        key0 = (gi < lr.n0 ? gi : lr.w0 + gi - lr.n0) * kGroup;
+      } else if (SEL) {
+        const int per = p.ps_shift - 4;
+        const int lp = sl[gi >> per];
+        if (lp < 0 || lp >= p.width) return;
+        key0 = (lp << p.ps_shift) + (gi & ((1 << per) - 1)) * kGroup;
+      } else {
+        key0 = gi * kGroup;
+      }
+      if (key0 < len) page = tab[key0 >> p.ps_shift];
+    };
+    auto issue = [&](int tt, int key0, int page) {
+      const int st = tt % kStages;
+      uint32_t mask = 0;
+      if (page >= 0 && page < p.n_pages) {
+        const int left = len - key0;
+        mask = left >= kGroup ? 0xFFFFu : (left > 0 ? (1u << left) - 1u : 0u);
+        if (local) {
+          const int below = p.n_sink - key0, from = lr.win_lo - key0;  // j < n_sink or j >= win_lo
+          const uint32_t sink = below >= kGroup ? 0xFFFFu : (below > 0 ? (1u << below) - 1u : 0u);
+          const uint32_t win = from <= 0 ? 0xFFFFu : (from < kGroup ? 0xFFFFu << from : 0u);
+          mask &= sink | win;
+        }
+      }
+      if (lane == 0) sm.mask[warp][st] = mask;
+      const int64_t at = mask ? (int64_t)page : 0;
+      const int row_in = key0 & ((1 << p.ps_shift) - 1);
+      const uint8_t* kb = p.kp.ptr + at * p.kp.page + row_in * p.kp.row + head * p.kp.head;
+      const uint8_t* vb = p.vp.ptr + at * p.vp.page + row_in * p.vp.row + head * p.vp.head;
+      const uint32_t ks = smem_u32(kst + st * kStageBytes), vs = smem_u32(vst + st * kStageBytes);
+      constexpr int kChunks = kRow / 16, kRows = 32 / kChunks;  // 16-byte chunks a row; rows a step
+#pragma unroll
+      for (int u = 0; u < kGroup / kRows; ++u) {
+        const int r = u * kRows + lane / kChunks, c = lane % kChunks;
+        const bool ok = (mask >> r) & 1u;  // other rows become zeros and are not read
+        const int ck = E4M3 ? c ^ ((r & 1) << 2) : c ^ (r & 7);
+        const int cv = E4M3 ? c ^ (((r >> 1) & 3) << 1) : c ^ (r & 7);
+        cp_async16(ks + r * kRow + ck * 16, ok ? kb + r * p.kp.row + c * 16 : p.kp.ptr, ok);
+        cp_async16(vs + r * kRow + cv * 16, ok ? vb + r * p.vp.row + c * 16 : p.vp.ptr, ok);
+      }
+    };
+
+    int key0, page;
+#pragma unroll 1
+    for (int s = 0; s < kStages - 1; ++s) {
+      locate(s, key0, page);
+      if (s < n_run) issue(s, key0, page);
+      cp_async_commit();
+    }
+    locate(kStages - 1, key0, page);
+#pragma unroll 1
+    for (int tt = 0; tt < n_run; ++tt) {
+      cp_async_wait<kStages - 2>();
+      __syncwarp();
+      if (tt + kStages - 1 < n_run) issue(tt + kStages - 1, key0, page);
+      cp_async_commit();
+      locate(tt + kStages, key0, page);  // its table entry arrives during this tile
+      const int st = tt % kStages;
+      const uint32_t mask = sm.mask[warp][st];
+      if (mask == 0u) continue;
+      const uint8_t* kt = kst + st * kStageBytes;
+      const uint8_t* vt = vst + st * kStageBytes;
+
+      // S: keys 0-7 and 8-15 of the group
+      float s[2][4] = {};
+      if (E4M3) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int r = n * 8 + g;
+            const uint4 w = *reinterpret_cast<const uint4*>(
+                kt + r * kRow + ((4 * j + t) ^ ((r & 1) << 2)) * 16);
+            const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              mma16816_f16(s[n], qa[4 * j + u], e4m3x2_to_f16x2((uint16_t)x[u]),
+                           e4m3x2_to_f16x2((uint16_t)(x[u] >> 16)));
+          }
+      } else {
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          const int q4 = lane >> 3, r = (lane & 7) + 8 * (q4 >> 1);
+          uint32_t w[4];
+          ldmatrix_x4(w, smem_u32(kt + r * kRow + (((2 * kk + (q4 & 1)) ^ (r & 7)) << 4)));
+          mma16816(s[0], qa[kk], w[0], w[1], s[0]);
+          mma16816(s[1], qa[kk], w[2], w[3], s[1]);
+        }
+      }
+      float tmax[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const bool ok = (mask >> (n * 8 + 2 * t + (e & 1))) & 1u;
+          const float x = ok ? s[n][e] * ms[e >> 1] : -INFINITY;
+          s[n][e] = x;
+          tmax[e >> 1] = fmaxf(tmax[e >> 1], x);
+        }
+      float alpha[2], ref[2];
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        const float mnew = fmaxf(mrow[hh], quad_max(tmax[hh]));
+        const float m0 = mnew == -INFINITY ? 0.f : mnew;  // nothing seen yet: every term is 0
+        alpha[hh] = exp2f(mrow[hh] - m0);
+        ref[hh] = E4M3 ? m0 - kPShift : m0;
+        mrow[hh] = mnew;
+      }
+      float pr[2][4];
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) pr[n][e] = exp2f(s[n][e] - ref[e >> 1]);
+      lrow[0] = lrow[0] * alpha[0] + ((pr[0][0] + pr[0][1]) + (pr[1][0] + pr[1][1]));
+      lrow[1] = lrow[1] * alpha[1] + ((pr[0][2] + pr[0][3]) + (pr[1][2] + pr[1][3]));
+      if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+        for (int d = 0; d < 16; ++d) {
+          oacc[d][0] *= alpha[0];
+          oacc[d][1] *= alpha[0];
+          oacc[d][2] *= alpha[1];
+          oacc[d][3] *= alpha[1];
+        }
+      }
+      uint32_t pa[4];
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        pa[2 * n] = E4M3 ? pack_f16x2(pr[n][0], pr[n][1]) : pack_bf16x2(pr[n][0], pr[n][1]);
+        pa[2 * n + 1] = E4M3 ? pack_f16x2(pr[n][2], pr[n][3]) : pack_bf16x2(pr[n][2], pr[n][3]);
+      }
+      if (E4M3) {
+        // the thread's keys 2t, 2t+1, 2t+8, 2t+9, dimensions 16 g .. 16 g + 15:
+        // product d takes dimension 16 n + d as its column n
+        uint4 w[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int r = 2 * t + (u & 1) + 8 * (u >> 1);
+          w[u] = *reinterpret_cast<const uint4*>(vt + r * kRow + ((g ^ (((r >> 1) & 3) << 1)) << 4));
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t x[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            x[u] = c == 0 ? w[u].x : c == 1 ? w[u].y : c == 2 ? w[u].z : w[u].w;
+          const uint32_t a0 = __byte_perm(x[0], x[1], 0x5140), a1 = __byte_perm(x[0], x[1], 0x7362);
+          const uint32_t b0 = __byte_perm(x[2], x[3], 0x5140), b1 = __byte_perm(x[2], x[3], 0x7362);
+          mma16816_f16(oacc[4 * c], pa, e4m3x2_to_f16x2((uint16_t)a0), e4m3x2_to_f16x2((uint16_t)b0));
+          mma16816_f16(oacc[4 * c + 1], pa, e4m3x2_to_f16x2((uint16_t)(a0 >> 16)),
+                       e4m3x2_to_f16x2((uint16_t)(b0 >> 16)));
+          mma16816_f16(oacc[4 * c + 2], pa, e4m3x2_to_f16x2((uint16_t)a1), e4m3x2_to_f16x2((uint16_t)b1));
+          mma16816_f16(oacc[4 * c + 3], pa, e4m3x2_to_f16x2((uint16_t)(a1 >> 16)),
+                       e4m3x2_to_f16x2((uint16_t)(b1 >> 16)));
+        }
+      } else {
+#pragma unroll
+        for (int dp = 0; dp < 8; ++dp) {
+          const int q4 = lane >> 3, r = (lane & 7) + 8 * (q4 & 1);
+          uint32_t w[4];
+          ldmatrix_x4_trans(w, smem_u32(vt + r * kRow + (((2 * dp + (q4 >> 1)) ^ (r & 7)) << 4)));
+          mma16816(oacc[2 * dp], pa, w[0], w[1], oacc[2 * dp]);
+          mma16816(oacc[2 * dp + 1], pa, w[2], w[3], oacc[2 * dp + 1]);
+        }
+      }
+    }
+    cp_async_wait<0>();
+    __syncwarp();
+
+    // ---- join the four warps; each leaves its rows in its own (now idle) stages
+    float* wo = reinterpret_cast<float*>(kst);
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh) {
+      const int r = g + 8 * hh;
+      const float l = quad_sum(lrow[hh]);
+      if (r < p.G) {
+        if (t == 0) {
+          sm.wm[warp][r] = mrow[hh];
+          sm.wl[warp][r] = l;
+        }
+#pragma unroll
+        for (int d = 0; d < 16; ++d) {
+          if (E4M3) {
+            wo[r * kD + (2 * t) * 16 + d] = oacc[d][2 * hh];
+            wo[r * kD + (2 * t + 1) * 16 + d] = oacc[d][2 * hh + 1];
+          } else {
+            wo[r * kD + 8 * d + 2 * t] = oacc[d][2 * hh];
+            wo[r * kD + 8 * d + 2 * t + 1] = oacc[d][2 * hh + 1];
+          }
+        }
+      }
+    }
+    __syncthreads();
+    const bool whole = t0 == 0 && t1 == tiles;
+    float* part = p.part + ((int64_t)blockIdx.x * 2 + (pos == start ? 0 : 1)) * p.G * kPartRow;
+    for (int r = 0; r < p.G; ++r) {
+      float M = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kAttnWarps; ++w) M = fmaxf(M, sm.wm[w][r]);
+      float o = 0.f, l = 0.f;
+#pragma unroll
+      for (int w = 0; w < kAttnWarps; ++w) {
+        // a warp that saw no key has l = 0 and o = 0; a NaN score leaves NaN in l and o
+        const float f = exp2f(sm.wm[w][r] - (M == -INFINITY ? 0.f : M) - (E4M3 ? kPShift : 0.f));
+        const float fw = sm.wm[w][r] == -INFINITY && sm.wl[w][r] == sm.wl[w][r] ? 0.f : f;
+        o += fw * reinterpret_cast<const float*>(&sm.w[w].k[0][0][0])[r * kD + tid];
+        l += fw * sm.wl[w][r];
+      }
+      if (whole) {
+        store_final(p, b, head, r, tid, M, l, o);
+      } else {
+        part[r * kPartRow + 4 + tid] = o;
+        if (tid == 0) {
+          part[r * kPartRow] = M;
+          part[r * kPartRow + 1] = l;
+        }
+      }
+    }
+    pos += n_run;
+    if (pos >= end) return;
+    __syncthreads();
+  }
+}
+
+// Joins a row's partials, in CTA order, one CTA per (request, kv head, query
+// head): warp w sums a quarter of them, lane i dimensions 4 i .. 4 i + 3.  Rows
+// without keys get zeros (lse -inf); rows that one CTA covered are done already.
+template <bool SEL>
+__global__ void __launch_bounds__(128) paged_join_kernel(const PagedAttnParams p) {
+  griddep_wait();
+  const int row = blockIdx.x, r = blockIdx.y, b = row / p.Hkv, i = row % p.Hkv;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tiles = tiles_of(row_groups<SEL>(p, b, i, paged_len(p, b)));
+  if (tiles == 0) {
+    store_final(p, b, p.head[i], r, tid, -INFINITY, 0.f, 0.f);
+    return;
+  }
+  const int64_t chunk = p.meta[0], first = p.meta[1 + (int64_t)row];
+  const int64_t c0 = first / chunk, c1 = (first + tiles - 1) / chunk;
+  if (c0 == c1) return;
+  const int n = (int)(c1 - c0 + 1);
+  // the first CTA's run starts inside its share unless the row starts there
+  const int64_t stride = (int64_t)p.G * kPartRow;
+  auto at = [&](int s) {
+    return p.part + ((c0 + s) * 2 + (s == 0 && first != c0 * chunk ? 1 : 0)) * stride + r * kPartRow;
+  };
+  __shared__ float sm_m[4], sm_l[4], sm_o[4][kD];
+  float M = -INFINITY;
+  for (int s = tid; s < n; s += 128) M = fmaxf(M, __ldcg(at(s)));
+  M = warp_max(M);
+  if (lane == 0) sm_m[warp] = M;
+  __syncthreads();
+  M = fmaxf(fmaxf(sm_m[0], sm_m[1]), fmaxf(sm_m[2], sm_m[3]));
+  const float m0 = M == -INFINITY ? 0.f : M;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.f;
+  const int s0 = (int)((int64_t)n * warp / 4), s1 = (int)((int64_t)n * (warp + 1) / 4);
+#pragma unroll 4
+  for (int s = s0; s < s1; ++s) {
+    const float* x = at(s);
+    const float2 ml = __ldcg(reinterpret_cast<const float2*>(x));
+    const float4 v = __ldcg(reinterpret_cast<const float4*>(x + 4 + 4 * lane));
+    const float f = ml.x == -INFINITY && ml.y == ml.y ? 0.f : exp2f(ml.x - m0);
+    l += f * ml.y;
+    acc.x += f * v.x;
+    acc.y += f * v.y;
+    acc.z += f * v.z;
+    acc.w += f * v.w;
+  }
+  reinterpret_cast<float4*>(sm_o[warp])[lane] = acc;
+  if (lane == 0) sm_l[warp] = l;
+  __syncthreads();
+  const float o = (sm_o[0][tid] + sm_o[1][tid]) + (sm_o[2][tid] + sm_o[3][tid]);
+  l = (sm_l[0] + sm_l[1]) + (sm_l[2] + sm_l[3]);
+  store_final(p, b, p.head[i], r, tid, M, l, o);
+}
+
+template <bool E4M3, bool SEL>
+rtp_status launch(const PagedAttnParams& p, int ctas, cudaStream_t s) {
+  const size_t smem = sizeof(AttnSmem<E4M3>);
+  if (cudaFuncSetAttribute(paged_attn_kernel<E4M3, SEL>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return RTP_ERR_CUDA;
+  rtp_status st;
+  {
+    TraceScope tr("paged_attn", s);
+    if ((st = check_cuda(launch_dependent(paged_attn_kernel<E4M3, SEL>, dim3(ctas),
+                                          dim3(kAttnThreads), smem, s, p))) != RTP_OK)
+      return st;
+  }
+  TraceScope tr("paged_join", s);
+  return check_cuda(launch_dependent(paged_join_kernel<SEL>, dim3(p.B * p.Hkv, p.G), dim3(128), 0,
+                                     s, p));
+}
+
+constexpr int kAttnCtas = 2 * 148;  // two CTAs on every SM
+
+struct AttnWs {
+  size_t meta, part, total;
+};
+AttnWs attn_ws(int32_t B, int32_t Hkv, int32_t G) {
+  AttnWs w;
+  w.meta = kStatusBytes;
+  w.part = align_up(w.meta + 8 * (1 + (size_t)B * Hkv), 256);
+  w.total = align_up(w.part + (size_t)kAttnCtas * 2 * G * kPartRow * 4, 256);
+  return w;
+}
+
+}  // namespace
+
+size_t paged_plan_ws(int32_t B);
+size_t paged_select_ws(int32_t rows, int32_t width);
+
+}  // namespace rtp
+
+using namespace rtp;
+
+extern "C" size_t rtp_paged_workspace_size(rtp_paged_op op, int32_t B, int32_t H, int32_t Hkv,
+                                           const uint8_t* kv_role, int32_t table_width) {
+  if (B < 0 || table_width < 0) return kStatusBytes;
+  if (op == RTP_PAGED_PLAN) return paged_plan_ws(B);
+  PagedHeads ph;
+  if (make_paged_heads(H, Hkv, kv_role, &ph) != RTP_OK) return kStatusBytes;
+  if (op == RTP_PAGED_SELECT) return paged_select_ws(B * ph.n_rkv, table_width);
+  if (op == RTP_PAGED_ATTN) return attn_ws(B, Hkv, ph.G).total;
+  return kStatusBytes;
+}
+
+extern "C" rtp_status rtp_paged_attn_decode(
+    int32_t B, int32_t H, int32_t Hkv, const uint8_t* kv_role, int32_t window, int32_t n_sink,
+    const void* q, int64_t q_stride, rtp_pages k_pages, rtp_pages v_pages, const float* k_scale,
+    const float* v_scale, const int32_t* block_table, int64_t table_stride, int32_t table_width,
+    const int32_t* seq_lens, const int32_t* sel, const int32_t* sel_count, int32_t n_sel,
+    float softmax_scale, void* o, int64_t o_stride, float* lse, void* ws, size_t ws_bytes,
+    rtp_stream_t stream) {
+  PagedHeads ph;
+  rtp_status st = make_paged_heads(H, Hkv, kv_role, &ph);
+  if (st != RTP_OK) return st;
+  if (B < 0 || table_width < 1 || table_stride < table_width) return RTP_ERR_INVALID_ARG;
+  if (ph.n_rkv < Hkv && (window < 1 || n_sink < 0)) return RTP_ERR_INVALID_ARG;
+  if (!(softmax_scale > 0.f) || !isfinite(softmax_scale)) return RTP_ERR_INVALID_ARG;
+  if ((sel == nullptr) != (sel_count == nullptr) || (sel != nullptr && n_sel < 1))
+    return RTP_ERR_INVALID_ARG;
+  if ((st = check_cache(k_pages, v_pages, k_scale, v_scale)) != RTP_OK) return st;
+  if ((int64_t)table_width * k_pages.page_size > kMaxTokens) return RTP_ERR_UNSUPPORTED;
+  if (sel != nullptr && (int64_t)n_sel * k_pages.page_size > kMaxTokens) return RTP_ERR_UNSUPPORTED;
+  if (B == 0) return RTP_OK;
+  if ((int64_t)B * Hkv > INT32_MAX / 4) return RTP_ERR_UNSUPPORTED;
+  if (q == nullptr || o == nullptr || block_table == nullptr || seq_lens == nullptr)
+    return RTP_ERR_INVALID_ARG;
+  if (q_stride < (int64_t)H * kD || o_stride < (int64_t)H * kD) return RTP_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(o) || (q_stride * 2) % 16 || (o_stride * 2) % 16 ||
+      !aligned16(ws))
+    return RTP_ERR_ALIGNMENT;
+  const AttnWs L = attn_ws(B, Hkv, ph.G);
+  if (ws == nullptr || ws_bytes < L.total) return RTP_ERR_WORKSPACE_TOO_SMALL;
+  PagedAttnParams p;
+  memset(&p, 0, sizeof(p));
+  p.q = static_cast<const uint16_t*>(q);
+  p.q_sb = q_stride;
+  p.o = static_cast<uint16_t*>(o);
+  p.o_sb = o_stride;
+  p.lse = lse;
+  p.kp = page_addr(k_pages);
+  p.vp = page_addr(v_pages);
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.table = block_table;
+  p.table_stride = table_stride;
+  p.seq_lens = seq_lens;
+  p.sel = sel;
+  p.sel_count = sel_count;
+  p.meta = reinterpret_cast<int64_t*>(static_cast<char*>(ws) + L.meta);
+  p.part = reinterpret_cast<float*>(static_cast<char*>(ws) + L.part);
+  p.scale_log2 = softmax_scale * kLog2e;
+  p.B = B;
+  p.G = ph.G;
+  p.Hkv = Hkv;
+  p.n_rkv = ph.n_rkv;
+  p.H = H;
+  p.n_pages = k_pages.n_pages;
+  p.width = table_width;
+  p.ps_shift = log2_exact(k_pages.page_size);
+  p.window = window;
+  p.n_sink = n_sink;
+  p.n_sel = n_sel;
+  memcpy(p.head, ph.head, sizeof(p.head));
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (k_pages.type == RTP_KV_E4M3)
+    return sel ? launch<true, true>(p, kAttnCtas, s) : launch<true, false>(p, kAttnCtas, s);
+  return sel ? launch<false, true>(p, kAttnCtas, s) : launch<false, false>(p, kAttnCtas, s);
+}

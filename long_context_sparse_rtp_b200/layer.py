@@ -7,12 +7,18 @@ prefill:  rtp_index_scores -> rtp_topp_select -> rtp_sparse_attn_prefill
 decode:   rtp_index_scores on the new token (q16 + k16 append into the cache)
           -> rtp_sparse_attn_decode (retrieval heads) and rtp_local_attn (local
           heads, Lq = 1) into one output.
+paged decode (requests of different lengths, PagedCache):
+          rtp_paged_plan -> rtp_paged_kv_append (or rtp_paged_kv_write, without
+          bounds) -> rtp_paged_block_select (where pages are selected) ->
+          rtp_paged_attn_decode, every head.
 Only sequencing and buffer allocation happen here; every step runs in librtp.so.
 """
 from __future__ import annotations
 
 import torch
 
+from .paged import (rtp_paged_attn_decode, rtp_paged_block_select, rtp_paged_kv_append,
+                    rtp_paged_kv_write, rtp_paged_plan)
 from .rtp import (rtp_index_scores, rtp_local_attn, rtp_local_attn_decode_ring,
                   rtp_local_ring_write, rtp_sparse_attn_decode, rtp_sparse_attn_decode_select,
                   rtp_sparse_attn_prefill, rtp_topp_select)
@@ -116,6 +122,86 @@ def _side_stream(device):
         s = torch.cuda.Stream(device=device)
         _side_streams[key] = s
     return s
+
+
+class PagedCache:
+    """One layer's KV cache in pages, for up to `batch` requests of up to max_len
+    tokens each: the pages, the block table, the lengths and the free pages, all
+    on the GPU.  dtype torch.bfloat16, or torch.float8_e4m3fn with fp32 scales per
+    kv head (k_scale, v_scale [Hkv]).  bounds=True keeps the page bounds that
+    rtp_paged_block_select reads."""
+
+    def __init__(self, n_pages, page_size, kv_role, *, batch, max_len, device,
+                 dtype=torch.bfloat16, k_scale=None, v_scale=None, bounds=True):
+        self.page_size, self.kv_role = page_size, tuple(int(x) for x in kv_role)
+        Hkv, n_rkv = len(self.kv_role), sum(self.kv_role)
+        self.k_scale, self.v_scale = k_scale, v_scale
+        self.k_pages = torch.zeros(n_pages, page_size, Hkv, 128, dtype=dtype, device=device)
+        self.v_pages = torch.zeros_like(self.k_pages)
+        i32 = dict(dtype=torch.int32, device=device)
+        self.block_table = torch.full((batch, -(-max_len // page_size)), -1, **i32)
+        self.seq_lens = torch.zeros(batch, **i32)
+        self.free_pages = torch.arange(n_pages - 1, -1, -1, **i32)  # page 0 is taken first
+        self.free_count = torch.full((1,), n_pages, **i32)
+        self.bounds = self.bound_scale = None
+        if bounds and n_rkv:
+            self.bounds = torch.zeros(n_pages, n_rkv, 2, 128, dtype=torch.int8, device=device)
+            self.bound_scale = torch.zeros(n_pages, n_rkv, dtype=torch.float32, device=device)
+
+    def append(self, k, v, n_new, *, release=None, row_tokens=0, stream=None):
+        """Takes n_new [batch] int32 new tokens per request: k, v [T, Hkv, 128], packed
+        in request order, or padded to row_tokens per request.  release [batch]
+        (bool or uint8): requests whose pages go back first.  Returns the plan
+        (rtp_paged_plan); plan["admitted"] says which requests were taken."""
+        plan = rtp_paged_plan(self.seq_lens, n_new, self.block_table, self.free_pages,
+                              self.free_count, page_size=self.page_size, max_tokens=k.shape[0],
+                              row_tokens=row_tokens, release=release,
+                              out=dict(seq_lens=self.seq_lens, free_count=self.free_count),
+                              stream=stream)
+        if self.bounds is None:
+            rtp_paged_kv_write(k, v, plan["slot_map"], self.k_pages, self.v_pages,
+                               k_scale=self.k_scale, v_scale=self.v_scale, stream=stream)
+        else:
+            rtp_paged_kv_append(k, v, plan["spans"], self.k_pages, self.v_pages, self.kv_role,
+                                self.bounds, self.bound_scale, k_scale=self.k_scale,
+                                v_scale=self.v_scale, stream=stream)
+        return plan
+
+    def attend(self, q, *, window=None, n_sink=0, n_sel=None, n_first=1, n_recent=1, scale=None,
+               o=None, lse=None, stream=None):
+        """Attention of q [batch, 1, H, 128] over the cache.  n_sel: the retrieval heads
+        attend to that many pages each (rtp_paged_block_select), else to every key.
+        Returns (o, lse, sel), sel = (pages, counts) or None."""
+        sel = count = None
+        if n_sel is not None and sum(self.kv_role):
+            if self.bounds is None:
+                raise ValueError("n_sel needs a cache with bounds")
+            sel, count = rtp_paged_block_select(
+                q, self.bounds, self.bound_scale, self.block_table, self.seq_lens, self.kv_role,
+                page_size=self.page_size, n_sel=n_sel, n_first=n_first, n_recent=n_recent,
+                stream=stream)
+        o, lse = rtp_paged_attn_decode(q, self.k_pages, self.v_pages, self.block_table,
+                                       self.seq_lens, self.kv_role, window=window, n_sink=n_sink,
+                                       sel=sel, sel_count=count, k_scale=self.k_scale,
+                                       v_scale=self.v_scale, scale=scale, o=o, lse=lse,
+                                       stream=stream)
+        return o, lse, None if sel is None else (sel, count)
+
+
+def rtp_layer_decode_paged(q, k_new, v_new, cache, n_new, *, window=None, n_sink=0, n_sel=None,
+                           n_first=1, n_recent=1, scale=None, release=None, o=None, lse=None,
+                           stream=None):
+    """One decode step of a batch over a PagedCache: the new tokens' rows into the
+    pages, then attention.  q [B, 1, H, 128], k_new, v_new [B, 1, Hkv, 128], n_new
+    [B] int32: 1 for a running request, 0 for an unused row of a padded batch.
+    Nothing is read on the host, so the step can be captured in a CUDA graph and
+    replayed: lengths, tables and pages advance on the device.  Returns dict(o,
+    lse, sel, plan)."""
+    plan = cache.append(k_new.flatten(0, 1), v_new.flatten(0, 1), n_new, release=release,
+                        row_tokens=1, stream=stream)
+    o, lse, sel = cache.attend(q, window=window, n_sink=n_sink, n_sel=n_sel, n_first=n_first,
+                               n_recent=n_recent, scale=scale, o=o, lse=lse, stream=stream)
+    return dict(o=o, lse=lse, sel=sel, plan=plan)
 
 
 class DecodeGraph:

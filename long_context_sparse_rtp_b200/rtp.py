@@ -39,6 +39,13 @@ class Shape(ctypes.Structure):
                 ("q_pos0", ctypes.c_int64)]
 
 
+class Pages(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("stride_page", ctypes.c_int64),
+                ("stride_row", ctypes.c_int64), ("stride_head", ctypes.c_int64),
+                ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("type", ctypes.c_int32)]
+
+
 class View(ctypes.Structure):
     _fields_ = [("ptr", ctypes.c_void_p), ("stride_b", ctypes.c_int64),
                 ("stride_l", ctypes.c_int64)]
@@ -79,6 +86,19 @@ def lib():
                 L.rtp_dense_attn.argtypes = [S, V, V, V, f32, V, P, P, sz, P]
                 L.rtp_local_attn_decode_noalloc.argtypes = [S, P, i32, i32, V, V, V, f32, V, P, P]
                 L.rtp_probe_ex2.argtypes = [i32, i32, P, P]
+                i64, G = ctypes.c_int64, Pages
+                L.rtp_paged_workspace_size.restype = sz
+                L.rtp_paged_workspace_size.argtypes = [ctypes.c_int, i32, i32, i32, P, i32]
+                L.rtp_paged_plan.argtypes = [i32, i32, i32, P, P, P, P, i64, i32, P, i32, P, i32,
+                                             i32, P, P, P, P, P, P, P, sz, P]
+                L.rtp_paged_kv_write.argtypes = [i32, i32, P, i64, P, i64, P, G, G, P, P, P]
+                L.rtp_paged_kv_append.argtypes = [i32, i32, P, P, i64, P, i64, P, i32, G, G, P, P,
+                                                  P, P, P]
+                L.rtp_paged_block_select.argtypes = [i32, i32, i32, P, P, i64, P, P, i32, i32, P,
+                                                     i64, i32, P, i32, i32, i32, P, P, P, sz, P]
+                L.rtp_paged_attn_decode.argtypes = [i32, i32, i32, P, i32, i32, P, i64, G, G, P, P,
+                                                    P, i64, i32, P, P, P, i32, f32, P, i64, P, P,
+                                                    sz, P]
                 L.rtp_status_string.restype = ctypes.c_char_p
                 L.rtp_status_string.argtypes = [ctypes.c_int]
                 L.rtp_get_device_status.argtypes = [P, P]
@@ -87,7 +107,9 @@ def lib():
                            "rtp_sparse_attn_prefill", "rtp_sparse_attn_decode",
                            "rtp_sparse_attn_decode_select", "rtp_local_attn",
                            "rtp_local_ring_write", "rtp_local_attn_decode_ring", "rtp_probe_ex2", "rtp_dense_attn", "rtp_get_device_status",
-                           "rtp_local_attn_decode_noalloc"):
+                           "rtp_local_attn_decode_noalloc", "rtp_paged_plan",
+                           "rtp_paged_kv_write", "rtp_paged_kv_append",
+                           "rtp_paged_block_select", "rtp_paged_attn_decode"):
                     getattr(L, fn).restype = ctypes.c_int
                 _lib = L
     return _lib

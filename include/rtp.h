@@ -380,7 +380,8 @@ RTP_API size_t rtp_paged_workspace_size(rtp_paged_op op, int32_t B, int32_t H, i
  *    index in the batch of the token in its first new row; page -1 behind the last.
  *    min(max_tokens, max_tokens / page_size + 2 B) spans always suffice; further
  *    ones are dropped.  16-byte aligned.
- * free_cap: entries of free_pages (pages released beyond it are dropped).
+ * free_cap: entries of free_pages (pages released beyond it are dropped).  With
+ * B = 0 nothing is enqueued and nothing written.
  * Workspace: rtp_paged_workspace_size(RTP_PAGED_PLAN, B, ...).
  */
 RTP_API rtp_status rtp_paged_plan(int32_t B, int32_t page_size, int32_t row_tokens,

@@ -1,4 +1,5 @@
-"""Build librtp.so in-tree with nvcc for sm_100a (no torch involved).
+"""Build librtp.so in-tree with nvcc for sm_100a (no torch involved), and the
+Python binding of its paged calls, _paged.so, with g++ against torch.
 
     python -m long_context_sparse_rtp_b200.build [--force]
 """
@@ -14,6 +15,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "librtp.so")
+BINDING = os.path.join(CSRC, "paged_binding.cpp")
+EXT = os.path.join(HERE, "_paged.so")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -37,7 +40,40 @@ def _stale() -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    deps = [BINDING, os.path.join(INCLUDE, "rtp.h")]
+    if not force and os.path.exists(EXT) and \
+            all(os.path.getmtime(d) <= os.path.getmtime(EXT) for d in deps):
+        return EXT
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths, library_paths
+    tmp = EXT + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", INCLUDE, "-isystem", sysconfig.get_paths()["include"]]
+    for d in include_paths(device_type="cuda"):
+        cmd += ["-isystem", d]
+    cmd += ["-o", tmp, BINDING]
+    for d in library_paths():
+        cmd += ["-L", d]
+    cmd += ["-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-ltorch", "-lc10_cuda", "-lc10",
+            "-L", HERE, "-l:librtp.so", "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd))
+    subprocess.check_call(cmd)
+    os.replace(tmp, EXT)
+    return EXT
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    build_lib(force, verbose)
+    build_binding(force, verbose)
+    return LIB
+
+
+def build_lib(force: bool = False, verbose: bool = False) -> str:
     if not force and not _stale():
         return LIB
     nvcc = os.environ.get("NVCC", "nvcc")

@@ -12,8 +12,14 @@
 //
 // Within a tile each of the 4 warps has a group of 16 keys, which lies in one
 // page, and its own ring of shared-memory stages filled by cp.async: no barrier
-// inside a run of tiles.  Tensor-core products have the G query heads as their
-// (up to 16) rows.  Bound by HBM: 4 G flops a byte of bf16 K/V.
+// inside a run of tiles.  The tensor-core products are K Q^T (16 keys by 8 heads)
+// and V^T P^T (16 dimensions by 8 heads), P^T passing between them by an 8x8
+// transpose in registers: G <= 8 heads cost half the products, exponentials and
+// accumulators of a form with the heads as 16 rows (128K x 8, 8-bit, all heads:
+// 240 us with heads as rows, 164 so; bf16 64 ragged requests: 113 and 98).
+// Bound by HBM: 4 G flops a byte of bf16 K/V.  Three stages a warp, two CTAs an SM
+// (bf16) or three (8 bits), keep 128 and 96 KB a SM in flight; two stages and three
+// CTAs are as fast for bf16, four CTAs or six stages slower for 8 bits (167-177).
 //
 // Rounding: scores, maxima, sums and outputs in fp32; P is rounded once to the
 // 16-bit type of the P V product (bf16 beside bf16 rows; fp16 beside 8-bit ones,
@@ -102,15 +108,36 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-constexpr float kPShift = 14.f;  // P is held as 2^14 p in fp16: subnormal only under 2^-28
+__device__ __forceinline__ float ex2(float x) {  // 2^x, relative error under 2^-22
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// The 8x8 16-bit matrix held one row per quad, transposed.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(x));
+  return r;
+}
+
+// The reference m of P = 2^(x - m) moves only when a score exceeds it by more
+// than 2^kGrow, so most groups need one vote instead of a reduction.  In fp16 P
+// is held as 2^kShift p: at most 2^(kGrow + kShift) = 2^14, and subnormal only
+// under 2^-22 of the reference.
+constexpr float kGrow = 6.f;
+template <bool E4M3>
+constexpr float kShift = E4M3 ? 8.f : 0.f;
+constexpr float kNoRef = -3.0e38f;  // no key seen: any score moves it
 
 // One warp's stages.  K rows: bf16 swizzled by row & 7 (ldmatrix), 8-bit by
 // (row & 1) << 2; V rows: bf16 by row & 7, 8-bit by ((row >> 1) & 3) << 1: each
 // makes the eight 16-byte reads of a quarter warp fall on different banks.
 template <bool E4M3>
 struct WarpStages {
-  static constexpr int kRow = E4M3 ? kD : 2 * kD;          // bytes
-  static constexpr int kStages = E4M3 ? 6 : 3;
+  static constexpr int kRow = E4M3 ? kD : 2 * kD;  // bytes
+  static constexpr int kStages = 3;
+  static constexpr int kCtasPerSm = E4M3 ? 3 : 2;
   uint8_t k[kStages][kGroup][kRow];
   uint8_t v[kStages][kGroup][kRow];
 };
@@ -137,8 +164,10 @@ __device__ __forceinline__ void store_final(const PagedAttnParams& p, int b, int
     p.lse[(int64_t)b * p.H + h] = l > 0.f || l != l ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
 
-template <bool E4M3, bool SEL>
-__global__ void __launch_bounds__(kAttnThreads) paged_attn_kernel(const PagedAttnParams p) {
+// NT: tiles of 8 query heads (1 for G <= 8).
+template <bool E4M3, bool SEL, int NT>
+__global__ void __launch_bounds__(kAttnThreads, WarpStages<E4M3>::kCtasPerSm)
+    paged_attn_kernel(const PagedAttnParams p) {
   griddep_wait();
   extern __shared__ __align__(128) unsigned char smem_raw[];
   AttnSmem<E4M3>& sm = *reinterpret_cast<AttnSmem<E4M3>*>(smem_raw);
@@ -166,10 +195,15 @@ __global__ void __launch_bounds__(kAttnThreads) paged_attn_kernel(const PagedAtt
     }
     return before + x - v;
   };
-  int64_t W = 0;
+  int64_t W = 0, mine = 0, before = 0;  // the first 128 requests' sums stay in registers
   for (int b0 = 0; b0 < p.B; b0 += kAttnThreads) {
     int64_t all;
-    scan(b0 + tid < p.B ? request_tiles<SEL>(p, b0 + tid) : 0, all);
+    const int64_t n = b0 + tid < p.B ? request_tiles<SEL>(p, b0 + tid) : 0;
+    const int64_t at = scan(n, all);
+    if (b0 == 0) {
+      mine = n;
+      before = at;
+    }
     W += all;
   }
   const int64_t chunk = max((int64_t)1, (W + gridDim.x - 1) / gridDim.x);
@@ -178,10 +212,12 @@ __global__ void __launch_bounds__(kAttnThreads) paged_attn_kernel(const PagedAtt
   const int64_t end = min(W, pos + chunk);
   if (pos >= end) return;
   for (int64_t b0 = 0, run = 0; b0 < p.B && run <= pos; b0 += kAttnThreads) {
-    int64_t all;
     const int b = (int)b0 + tid;
-    const int64_t n = b < p.B ? request_tiles<SEL>(p, b) : 0;
-    const int64_t at = run + scan(n, all);
+    int64_t n = mine, at = before, all = 0;
+    if (p.B > kAttnThreads) {
+      n = b < p.B ? request_tiles<SEL>(p, b) : 0;
+      at = run + scan(n, all);
+    }
     if (at <= pos && pos < at + n) {
       sm.req = b;
       sm.first = at;
@@ -197,6 +233,9 @@ __global__ void __launch_bounds__(kAttnThreads) paged_attn_kernel(const PagedAtt
   uint8_t* const kst = &sm.w[warp].k[0][0][0];
   uint8_t* const vst = &sm.w[warp].v[0][0][0];
   constexpr int kStageBytes = kGroup * kRow;
+  constexpr int kChunks = kRow / 16, kRows = 32 / kChunks;  // 16-byte chunks a row; rows a step
+  const int lr_ = lane / kChunks, lc = lane % kChunks;      // this lane's row of a step and chunk
+  const int64_t k_lane = lr_ * p.kp.row + lc * 16, v_lane = lr_ * p.vp.row + lc * 16;
 
   for (;;) {
     // ---- the row that holds tile `pos`
@@ -215,54 +254,6 @@ __global__ void __launch_bounds__(kAttnThreads) paged_attn_kernel(const PagedAtt
     const LocalRange lr = local_range(p, len);
     const bool local = i >= p.n_rkv;
     if (t0 == 0 && tid == 0) p.meta[1 + (int64_t)b * p.Hkv + i] = pos;
-
-    // ---- query rows g and g + 8 as product operands
-    uint32_t qa[8][4];
-    float ms[2] = {p.scale_log2, p.scale_log2};  // score multiplier of each row
-    {
-      const uint16_t* qb = p.q + b * p.q_sb + (int64_t)head * p.G * kD;
-#pragma unroll
-      for (int kk = 0; kk < 8; ++kk)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = g + 8 * (e & 1);
-          // 8-bit rows are read 16 bytes a thread: product kk of 16 bytes j takes
-          // dimensions 64 j + 16 t + 4 (kk % 4) + {0, 1 | 2, 3}
-          const int d = E4M3 ? 64 * (kk >> 2) + 16 * t + 4 * (kk & 3) + 2 * (e >> 1)
-                             : 16 * kk + 8 * (e >> 1) + 2 * t;
-          qa[kk][e] = r < p.G ? *reinterpret_cast<const uint32_t*>(qb + r * kD + d) : 0u;
-        }
-      if (E4M3) {
-        const float ks = p.k_scale ? p.k_scale[head] : 1.f;
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          float a = 0.f;
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-#pragma unroll
-            for (int e = hh; e < 4; e += 2)
-              a = fmaxf(a, fmaxf(fabsf(bf16_lo(qa[kk][e])), fabsf(bf16_hi(qa[kk][e]))));
-          a = quad_max(a);
-          int ex = (int)((__float_as_uint(a) >> 23) & 0xFF) - 127;
-          ex = a > 0.f ? max(-100, min(ex, 127)) : 14;
-          const float up = __uint_as_float((uint32_t)(14 - ex + 127) << 23);
-          ms[hh] *= ks * __uint_as_float((uint32_t)(ex - 14 + 127) << 23);
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-#pragma unroll
-            for (int e = hh; e < 4; e += 2)
-              qa[kk][e] = pack_f16x2(bf16_lo(qa[kk][e]) * up, bf16_hi(qa[kk][e]) * up);
-        }
-      }
-    }
-
-    float oacc[16][4];
-#pragma unroll
-    for (int d = 0; d < 16; ++d)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) oacc[d][e] = 0.f;
-    float mrow[2] = {-INFINITY, -INFINITY};
-    float lrow[2] = {0.f, 0.f};
 
     // ---- this warp's groups: tile tt of the run is group 4 (t0 + tt) + warp
     const int n_run = t1 - t0;
@@ -286,8 +277,9 @@ __global__ void __launch_bounds__(kAttnThreads) paged_attn_kernel(const PagedAtt
       }
       if (key0 < len) page = tab[key0 >> p.ps_shift];
     };
-    auto issue = [&](int tt, int key0, int page) {
-      const int st = tt % kStages;
+    const uint8_t* const khead = p.kp.ptr + head * p.kp.head + k_lane;
+    const uint8_t* const vhead = p.vp.ptr + head * p.vp.head + v_lane;
+    auto issue = [&](int st, int key0, int page) {
       uint32_t mask = 0;
       if (page >= 0 && page < p.n_pages) {
         const int left = len - key0;
@@ -300,20 +292,21 @@ __global__ void __launch_bounds__(kAttnThreads) paged_attn_kernel(const PagedAtt
         }
       }
       if (lane == 0) sm.mask[warp][st] = mask;
-      const int64_t at = mask ? (int64_t)page : 0;
+      if (mask == 0) return;  // nothing to load and nothing read
       const int row_in = key0 & ((1 << p.ps_shift) - 1);
-      const uint8_t* kb = p.kp.ptr + at * p.kp.page + row_in * p.kp.row + head * p.kp.head;
-      const uint8_t* vb = p.vp.ptr + at * p.vp.page + row_in * p.vp.row + head * p.vp.head;
+      const uint8_t* kb = khead + (int64_t)page * p.kp.page + row_in * p.kp.row;
+      const uint8_t* vb = vhead + (int64_t)page * p.vp.page + row_in * p.vp.row;
       const uint32_t ks = smem_u32(kst + st * kStageBytes), vs = smem_u32(vst + st * kStageBytes);
-      constexpr int kChunks = kRow / 16, kRows = 32 / kChunks;  // 16-byte chunks a row; rows a step
 #pragma unroll
       for (int u = 0; u < kGroup / kRows; ++u) {
-        const int r = u * kRows + lane / kChunks, c = lane % kChunks;
+        const int r = u * kRows + lr_;
         const bool ok = (mask >> r) & 1u;  // other rows become zeros and are not read
-        const int ck = E4M3 ? c ^ ((r & 1) << 2) : c ^ (r & 7);
-        const int cv = E4M3 ? c ^ (((r >> 1) & 3) << 1) : c ^ (r & 7);
-        cp_async16(ks + r * kRow + ck * 16, ok ? kb + r * p.kp.row + c * 16 : p.kp.ptr, ok);
-        cp_async16(vs + r * kRow + cv * 16, ok ? vb + r * p.vp.row + c * 16 : p.vp.ptr, ok);
+        const int ck = E4M3 ? lc ^ ((r & 1) << 2) : lc ^ (r & 7);
+        const int cv = E4M3 ? lc ^ (((r >> 1) & 3) << 1) : lc ^ (r & 7);
+        cp_async16(ks + r * kRow + ck * 16, kb, ok);
+        cp_async16(vs + r * kRow + cv * 16, vb, ok);
+        kb += kRows * p.kp.row;
+        vb += kRows * p.vp.row;
       }
     };
 
@@ -325,118 +318,195 @@ __global__ void __launch_bounds__(kAttnThreads) paged_attn_kernel(const PagedAtt
       cp_async_commit();
     }
     locate(kStages - 1, key0, page);
+
+    // ---- query heads nt * 8 + g as product operands (columns; keys are the rows)
+    uint32_t qb[NT][8][2];
+    float ms[NT][2];  // score multipliers of this thread's columns, heads nt * 8 + 2 t + {0, 1}
+    {
+      const uint16_t* q = p.q + b * p.q_sb + (int64_t)head * p.G * kD;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int r = nt * 8 + g;
+            // 8-bit rows are read 16 bytes a thread: product 4 j + u takes dimensions
+            // 64 j + 16 t + 4 u + {0, 1 | 2, 3}
+            const int d = E4M3 ? 64 * (kk >> 2) + 16 * t + 4 * (kk & 3) + 2 * e
+                               : 16 * kk + 8 * e + 2 * t;
+            qb[nt][kk][e] = r < p.G ? *reinterpret_cast<const uint32_t*>(q + r * kD + d) : 0u;
+          }
+        ms[nt][0] = ms[nt][1] = p.scale_log2;
+        if (E4M3) {
+          float a = 0.f;
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              a = fmaxf(a, fmaxf(fabsf(bf16_lo(qb[nt][kk][e])), fabsf(bf16_hi(qb[nt][kk][e]))));
+          a = quad_max(a);
+          int ex = (int)((__float_as_uint(a) >> 23) & 0xFF) - 127;
+          ex = a > 0.f ? max(-100, min(ex, 127)) : 14;
+          const float up = __uint_as_float((uint32_t)(14 - ex + 127) << 23);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              qb[nt][kk][e] = pack_f16x2(bf16_lo(qb[nt][kk][e]) * up, bf16_hi(qb[nt][kk][e]) * up);
+          const float down = p.scale_log2 * (p.k_scale ? p.k_scale[head] : 1.f) *
+                             __uint_as_float((uint32_t)(ex - 14 + 127) << 23);
+          ms[nt][0] = __shfl_sync(0xffffffffu, down, 8 * t);
+          ms[nt][1] = __shfl_sync(0xffffffffu, down, 8 * t + 4);
+        }
+      }
+    }
+
+    // o: 8 tiles of 16 dimensions (rows) x 8 heads (columns)
+    float oacc[NT][8][4];
+    float nref[NT][2], lsum[NT][2];  // kShift - m, and this thread's share of the sum
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int d = 0; d < 8; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) oacc[nt][d][e] = 0.f;
+      nref[nt][0] = nref[nt][1] = -kNoRef;
+      lsum[nt][0] = lsum[nt][1] = 0.f;
+    }
+
+    int st = 0, st_in = kStages - 1;  // stage of this tile, and of the one to load
 #pragma unroll 1
     for (int tt = 0; tt < n_run; ++tt) {
       cp_async_wait<kStages - 2>();
       __syncwarp();
-      if (tt + kStages - 1 < n_run) issue(tt + kStages - 1, key0, page);
+      if (tt + kStages - 1 < n_run) issue(st_in, key0, page);
       cp_async_commit();
       locate(tt + kStages, key0, page);  // its table entry arrives during this tile
-      const int st = tt % kStages;
       const uint32_t mask = sm.mask[warp][st];
-      if (mask == 0u) continue;
       const uint8_t* kt = kst + st * kStageBytes;
       const uint8_t* vt = vst + st * kStageBytes;
+      st = st == kStages - 1 ? 0 : st + 1;
+      st_in = st_in == kStages - 1 ? 0 : st_in + 1;
+      if (mask == 0u) continue;
 
-      // S: keys 0-7 and 8-15 of the group
-      float s[2][4] = {};
+      // S: 16 keys (rows) x 8 heads; this thread has keys g and g + 8
+      float s[NT][4] = {};
       if (E4M3) {
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int j = 0; j < 2; ++j) {
+          const uint8_t* at = kt + g * kRow + ((4 * j + t) ^ ((g & 1) << 2)) * 16;
+          const uint4 w0 = *reinterpret_cast<const uint4*>(at);
+          const uint4 w1 = *reinterpret_cast<const uint4*>(at + 8 * kRow);
+          const uint32_t x0[4] = {w0.x, w0.y, w0.z, w0.w}, x1[4] = {w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int r = n * 8 + g;
-            const uint4 w = *reinterpret_cast<const uint4*>(
-                kt + r * kRow + ((4 * j + t) ^ ((r & 1) << 2)) * 16);
-            const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+          for (int u = 0; u < 4; ++u) {
+            const uint32_t a[4] = {
+                e4m3x2_to_f16x2((uint16_t)x0[u]), e4m3x2_to_f16x2((uint16_t)x1[u]),
+                e4m3x2_to_f16x2((uint16_t)(x0[u] >> 16)), e4m3x2_to_f16x2((uint16_t)(x1[u] >> 16))};
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-              mma16816_f16(s[n], qa[4 * j + u], e4m3x2_to_f16x2((uint16_t)x[u]),
-                           e4m3x2_to_f16x2((uint16_t)(x[u] >> 16)));
+            for (int nt = 0; nt < NT; ++nt)
+              mma16816_f16(s[nt], a, qb[nt][4 * j + u][0], qb[nt][4 * j + u][1]);
           }
+        }
       } else {
+        const int r = lane & 15;
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) {
-          const int q4 = lane >> 3, r = (lane & 7) + 8 * (q4 >> 1);
-          uint32_t w[4];
-          ldmatrix_x4(w, smem_u32(kt + r * kRow + (((2 * kk + (q4 & 1)) ^ (r & 7)) << 4)));
-          mma16816(s[0], qa[kk], w[0], w[1], s[0]);
-          mma16816(s[1], qa[kk], w[2], w[3], s[1]);
+          uint32_t a[4];
+          ldmatrix_x4(a, smem_u32(kt + r * kRow + (((2 * kk + (lane >> 4)) ^ (r & 7)) << 4)));
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma16816(s[nt], a, qb[nt][kk][0], qb[nt][kk][1], s[nt]);
         }
       }
-      float tmax[2] = {-INFINITY, -INFINITY};
+      if (mask != 0xFFFFu) {
+        const bool ok0 = (mask >> g) & 1u, ok1 = (mask >> (g + 8)) & 1u;
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+        for (int nt = 0; nt < NT; ++nt) {
+          // the multipliers are positive
+          if (!ok0) s[nt][0] = s[nt][1] = -INFINITY;
+          if (!ok1) s[nt][2] = s[nt][3] = -INFINITY;
+        }
+      }
+      float y[NT][4];
+      bool grow = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const bool ok = (mask >> (n * 8 + 2 * t + (e & 1))) & 1u;
-          const float x = ok ? s[n][e] * ms[e >> 1] : -INFINITY;
-          s[n][e] = x;
-          tmax[e >> 1] = fmaxf(tmax[e >> 1], x);
+          y[nt][e] = fmaf(s[nt][e], ms[nt][e & 1], nref[nt][e & 1]);
+          grow |= y[nt][e] > kGrow + kShift<E4M3>;
         }
-      float alpha[2], ref[2];
+      if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        const float mnew = fmaxf(mrow[hh], quad_max(tmax[hh]));
-        const float m0 = mnew == -INFINITY ? 0.f : mnew;  // nothing seen yet: every term is 0
-        alpha[hh] = exp2f(mrow[hh] - m0);
-        ref[hh] = E4M3 ? m0 - kPShift : m0;
-        mrow[hh] = mnew;
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float m = fmaxf(s[nt][c], s[nt][2 + c]) * ms[nt][c];
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+            const float to = fminf(nref[nt][c], kShift<E4M3> - m);
+            const float alpha = ex2(to - nref[nt][c]);
+            nref[nt][c] = to;
+            lsum[nt][c] *= alpha;
+#pragma unroll
+            for (int d = 0; d < 8; ++d) {
+              oacc[nt][d][c] *= alpha;
+              oacc[nt][d][2 + c] *= alpha;
+            }
+            y[nt][c] = fmaf(s[nt][c], ms[nt][c], to);
+            y[nt][2 + c] = fmaf(s[nt][2 + c], ms[nt][c], to);
+          }
       }
-      float pr[2][4];
+      uint32_t pb[NT][2];
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+      for (int nt = 0; nt < NT; ++nt) {
+        float pr[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) pr[n][e] = exp2f(s[n][e] - ref[e >> 1]);
-      lrow[0] = lrow[0] * alpha[0] + ((pr[0][0] + pr[0][1]) + (pr[1][0] + pr[1][1]));
-      lrow[1] = lrow[1] * alpha[1] + ((pr[0][2] + pr[0][3]) + (pr[1][2] + pr[1][3]));
-      if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
-#pragma unroll
-        for (int d = 0; d < 16; ++d) {
-          oacc[d][0] *= alpha[0];
-          oacc[d][1] *= alpha[0];
-          oacc[d][2] *= alpha[1];
-          oacc[d][3] *= alpha[1];
-        }
-      }
-      uint32_t pa[4];
-#pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        pa[2 * n] = E4M3 ? pack_f16x2(pr[n][0], pr[n][1]) : pack_bf16x2(pr[n][0], pr[n][1]);
-        pa[2 * n + 1] = E4M3 ? pack_f16x2(pr[n][2], pr[n][3]) : pack_bf16x2(pr[n][2], pr[n][3]);
+        for (int e = 0; e < 4; ++e) pr[e] = ex2(y[nt][e]);
+        lsum[nt][0] += pr[0] + pr[2];
+        lsum[nt][1] += pr[1] + pr[3];
+        pb[nt][0] = transpose8x8(E4M3 ? pack_f16x2(pr[0], pr[1]) : pack_bf16x2(pr[0], pr[1]));
+        pb[nt][1] = transpose8x8(E4M3 ? pack_f16x2(pr[2], pr[3]) : pack_bf16x2(pr[2], pr[3]));
       }
       if (E4M3) {
         // the thread's keys 2t, 2t+1, 2t+8, 2t+9, dimensions 16 g .. 16 g + 15:
-        // product d takes dimension 16 n + d as its column n
+        // product d takes dimensions 16 n + 2 d (its row n) and 16 n + 2 d + 1 (n + 8)
         uint4 w[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int r = 2 * t + (u & 1) + 8 * (u >> 1);
-          w[u] = *reinterpret_cast<const uint4*>(vt + r * kRow + ((g ^ (((r >> 1) & 3) << 1)) << 4));
-        }
+        for (int u = 0; u < 4; ++u)
+          w[u] = *reinterpret_cast<const uint4*>(vt + (2 * t + (u & 1) + 8 * (u >> 1)) * kRow +
+                                                 ((g ^ (t << 1)) << 4));
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t x[4];
 #pragma unroll
           for (int u = 0; u < 4; ++u)
             x[u] = c == 0 ? w[u].x : c == 1 ? w[u].y : c == 2 ? w[u].z : w[u].w;
-          const uint32_t a0 = __byte_perm(x[0], x[1], 0x5140), a1 = __byte_perm(x[0], x[1], 0x7362);
-          const uint32_t b0 = __byte_perm(x[2], x[3], 0x5140), b1 = __byte_perm(x[2], x[3], 0x7362);
-          mma16816_f16(oacc[4 * c], pa, e4m3x2_to_f16x2((uint16_t)a0), e4m3x2_to_f16x2((uint16_t)b0));
-          mma16816_f16(oacc[4 * c + 1], pa, e4m3x2_to_f16x2((uint16_t)(a0 >> 16)),
-                       e4m3x2_to_f16x2((uint16_t)(b0 >> 16)));
-          mma16816_f16(oacc[4 * c + 2], pa, e4m3x2_to_f16x2((uint16_t)a1), e4m3x2_to_f16x2((uint16_t)b1));
-          mma16816_f16(oacc[4 * c + 3], pa, e4m3x2_to_f16x2((uint16_t)(a1 >> 16)),
-                       e4m3x2_to_f16x2((uint16_t)(b1 >> 16)));
+#pragma unroll
+          for (int hlf = 0; hlf < 2; ++hlf) {
+            const uint32_t sel = hlf ? 0x7362u : 0x5140u;
+            const uint32_t lo = __byte_perm(x[0], x[1], sel), hi = __byte_perm(x[2], x[3], sel);
+            const uint32_t a[4] = {
+                e4m3x2_to_f16x2((uint16_t)lo), e4m3x2_to_f16x2((uint16_t)(lo >> 16)),
+                e4m3x2_to_f16x2((uint16_t)hi), e4m3x2_to_f16x2((uint16_t)(hi >> 16))};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma16816_f16(oacc[nt][2 * c + hlf], a, pb[nt][0], pb[nt][1]);
+          }
         }
       } else {
+        const int r = (lane & 7) + 8 * (lane >> 4);  // matrices: keys lo, dims lo | dims hi; keys hi ...
 #pragma unroll
-        for (int dp = 0; dp < 8; ++dp) {
-          const int q4 = lane >> 3, r = (lane & 7) + 8 * (q4 & 1);
-          uint32_t w[4];
-          ldmatrix_x4_trans(w, smem_u32(vt + r * kRow + (((2 * dp + (q4 >> 1)) ^ (r & 7)) << 4)));
-          mma16816(oacc[2 * dp], pa, w[0], w[1], oacc[2 * dp]);
-          mma16816(oacc[2 * dp + 1], pa, w[2], w[3], oacc[2 * dp + 1]);
+        for (int d = 0; d < 8; ++d) {
+          uint32_t a[4];
+          ldmatrix_x4_trans(
+              a, smem_u32(vt + r * kRow + (((2 * d + ((lane >> 3) & 1)) ^ (r & 7)) << 4)));
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma16816(oacc[nt][d], a, pb[nt][0], pb[nt][1], oacc[nt][d]);
         }
       }
     }
@@ -446,26 +516,26 @@ __global__ void __launch_bounds__(kAttnThreads) paged_attn_kernel(const PagedAtt
     // ---- join the four warps; each leaves its rows in its own (now idle) stages
     float* wo = reinterpret_cast<float*>(kst);
 #pragma unroll
-    for (int hh = 0; hh < 2; ++hh) {
-      const int r = g + 8 * hh;
-      const float l = quad_sum(lrow[hh]);
-      if (r < p.G) {
-        if (t == 0) {
-          sm.wm[warp][r] = mrow[hh];
-          sm.wl[warp][r] = l;
-        }
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int d = 0; d < 16; ++d) {
-          if (E4M3) {
-            wo[r * kD + (2 * t) * 16 + d] = oacc[d][2 * hh];
-            wo[r * kD + (2 * t + 1) * 16 + d] = oacc[d][2 * hh + 1];
-          } else {
-            wo[r * kD + 8 * d + 2 * t] = oacc[d][2 * hh];
-            wo[r * kD + 8 * d + 2 * t + 1] = oacc[d][2 * hh + 1];
+      for (int c = 0; c < 2; ++c) {
+        float l = lsum[nt][c];
+        l += __shfl_xor_sync(0xffffffffu, l, 4);
+        l += __shfl_xor_sync(0xffffffffu, l, 8);
+        l += __shfl_xor_sync(0xffffffffu, l, 16);
+        const int r = nt * 8 + 2 * t + c;
+        if (r < p.G) {
+          if (g == 0) {
+            sm.wm[warp][r] = nref[nt][c] == -kNoRef ? -INFINITY : kShift<E4M3> - nref[nt][c];
+            sm.wl[warp][r] = l;
+          }
+#pragma unroll
+          for (int d = 0; d < 8; ++d) {
+            wo[r * kD + (E4M3 ? 16 * g + 2 * d : 16 * d + g)] = oacc[nt][d][c];
+            wo[r * kD + (E4M3 ? 16 * g + 2 * d + 1 : 16 * d + g + 8)] = oacc[nt][d][2 + c];
           }
         }
       }
-    }
     __syncthreads();
     const bool whole = t0 == 0 && t1 == tiles;
     float* part = p.part + ((int64_t)blockIdx.x * 2 + (pos == start ? 0 : 1)) * p.G * kPartRow;
@@ -477,7 +547,7 @@ __global__ void __launch_bounds__(kAttnThreads) paged_attn_kernel(const PagedAtt
 #pragma unroll
       for (int w = 0; w < kAttnWarps; ++w) {
         // a warp that saw no key has l = 0 and o = 0; a NaN score leaves NaN in l and o
-        const float f = exp2f(sm.wm[w][r] - (M == -INFINITY ? 0.f : M) - (E4M3 ? kPShift : 0.f));
+        const float f = ex2(sm.wm[w][r] - (M == -INFINITY ? 0.f : M) - kShift<E4M3>);
         const float fw = sm.wm[w][r] == -INFINITY && sm.wl[w][r] == sm.wl[w][r] ? 0.f : f;
         o += fw * reinterpret_cast<const float*>(&sm.w[w].k[0][0][0])[r * kD + tid];
         l += fw * sm.wl[w][r];
@@ -551,17 +621,23 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const PagedAttnParams p
   store_final(p, b, p.head[i], r, tid, M, l, o);
 }
 
-template <bool E4M3, bool SEL>
-rtp_status launch(const PagedAttnParams& p, int ctas, cudaStream_t s) {
+constexpr int kSms = 148;
+constexpr int kMaxAttnCtas = 3 * kSms;
+
+template <bool E4M3, bool SEL, int NT>
+rtp_status launch(const PagedAttnParams& p, cudaStream_t s) {
   const size_t smem = sizeof(AttnSmem<E4M3>);
-  if (cudaFuncSetAttribute(paged_attn_kernel<E4M3, SEL>,
-                           cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+  constexpr int ctas = WarpStages<E4M3>::kCtasPerSm * kSms;
+  static_assert(ctas <= kMaxAttnCtas, "the workspace holds every CTA's partials");
+  auto* kernel = paged_attn_kernel<E4M3, SEL, NT>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
+      cudaSuccess)
     return RTP_ERR_CUDA;
   rtp_status st;
   {
     TraceScope tr("paged_attn", s);
-    if ((st = check_cuda(launch_dependent(paged_attn_kernel<E4M3, SEL>, dim3(ctas),
-                                          dim3(kAttnThreads), smem, s, p))) != RTP_OK)
+    if ((st = check_cuda(launch_dependent(kernel, dim3(ctas), dim3(kAttnThreads), smem, s, p))) !=
+        RTP_OK)
       return st;
   }
   TraceScope tr("paged_join", s);
@@ -569,7 +645,10 @@ rtp_status launch(const PagedAttnParams& p, int ctas, cudaStream_t s) {
                                      s, p));
 }
 
-constexpr int kAttnCtas = 2 * 148;  // two CTAs on every SM
+template <bool E4M3, bool SEL>
+rtp_status launch(const PagedAttnParams& p, cudaStream_t s) {
+  return p.G <= 8 ? launch<E4M3, SEL, 1>(p, s) : launch<E4M3, SEL, 2>(p, s);
+}
 
 struct AttnWs {
   size_t meta, part, total;
@@ -578,7 +657,7 @@ AttnWs attn_ws(int32_t B, int32_t Hkv, int32_t G) {
   AttnWs w;
   w.meta = kStatusBytes;
   w.part = align_up(w.meta + 8 * (1 + (size_t)B * Hkv), 256);
-  w.total = align_up(w.part + (size_t)kAttnCtas * 2 * G * kPartRow * 4, 256);
+  w.total = align_up(w.part + (size_t)kMaxAttnCtas * 2 * G * kPartRow * 4, 256);
   return w;
 }
 
@@ -663,6 +742,6 @@ extern "C" rtp_status rtp_paged_attn_decode(
   memcpy(p.head, ph.head, sizeof(p.head));
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (k_pages.type == RTP_KV_E4M3)
-    return sel ? launch<true, true>(p, kAttnCtas, s) : launch<true, false>(p, kAttnCtas, s);
-  return sel ? launch<false, true>(p, kAttnCtas, s) : launch<false, false>(p, kAttnCtas, s);
+    return sel ? launch<true, true>(p, s) : launch<true, false>(p, s);
+  return sel ? launch<false, true>(p, s) : launch<false, false>(p, s);
 }

@@ -6,20 +6,28 @@
 //   I(h, p) = sum_d max(q8_hd lo8_pd, q8_hd hi8_pd)
 //           = sum_d min(q8_hd, 0) lo8_pd + max(q8_hd, 0) hi8_pd,
 //   score = float(I) * (sq_h * s_p), and the largest over a kv head's G heads.
-// |I| <= 128 * 127 * 127 < 2^24, so I is exact in the 32-bit sums of the integer
-// tensor-core products and in fp32: every order of summation gives the same
-// score, and the selection (score descending, index ascending) is the same on
-// every run.  With sq * [lo8, hi8] * s_p bounding the page's keys, the score
+// |I| <= 128 * 127 * 127 < 2^24: with 8-bit values in fp16 and fp32 sums the
+// tensor-core products give I exactly, whatever the order of summation, so the
+// selection (score descending, index ascending) is the same on every run.
+// (The integer form of those products is far slower here: 96 rows of up to 2048
+// pages took 16 us with it, traced.)  With sq * [lo8, hi8] * s_p bounding the page's keys, the score
 // bounds every q . k of the page up to the rounding of q.
 //
 // paged_score_kernel reads the bounds once (2 x 128 bytes and a scale a page,
 // straight into fragments: bound by HBM); paged_topn_kernel finds the n-th
-// largest key of a row bit by bit with the row's keys in registers, and writes
-// the kept pages in order.
+// largest key of a row with the row's keys in registers, and writes the kept
+// pages in order.
+#include <algorithm>
+
 #include "paged.cuh"
 
 namespace rtp {
 namespace {
+
+// The score of an ordered key (score_key's inverse).
+__device__ __forceinline__ float key_score(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
+}
 
 struct SelectParams {
   const uint16_t* q; int64_t q_sb;
@@ -39,121 +47,161 @@ __device__ __forceinline__ int blocks_of(const SelectParams& p, int b) {
   return (int)min((int64_t)p.width, (len + (1 << p.ps_shift) - 1) >> p.ps_shift);
 }
 
-// D(16x8) += A(16x32 s8, row) * B(32x8 s8, col), 32-bit sums.
-__device__ __forceinline__ void mma_s8(int32_t (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                       uint32_t b1) {
+// D(16x8) += A(16x16 fp16, row) * B(16x8 fp16, col), fp32 sums.
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 "
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
       "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
-      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Four signed bytes as fp16, the first two in lo, the others in hi: exact (a byte
+// + 128 is the low mantissa of 1024 + byte + 128).
+__device__ __forceinline__ void s8x4_to_f16(uint32_t x, uint32_t& lo, uint32_t& hi) {
+  const __half2 off = __half2half2(__ushort_as_half(0x6480));  // 1152
+  x ^= 0x80808080u;
+  lo = __byte_perm(x, 0x64646464u, 0x4140);
+  hi = __byte_perm(x, 0x64646464u, 0x4342);
+  const __half2 l = __hsub2(*reinterpret_cast<__half2*>(&lo), off);
+  const __half2 h = __hsub2(*reinterpret_cast<__half2*>(&hi), off);
+  lo = *reinterpret_cast<const uint32_t*>(&l);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
 }
 
 constexpr int kScoreThreads = 256;
-constexpr int kScoreSteps = 2;                                    // 8-page steps per warp
-constexpr int kScorePages = kScoreSteps * 8 * kScoreThreads / 32;  // pages of a CTA
+constexpr int kScorePages = 16 * kScoreThreads / 32;  // pages of a CTA at once, 16 a warp
+constexpr int kQRow = kD + 4;  // fp16 elements: eight bytes of padding keep reads on all banks
 
-__global__ void __launch_bounds__(kScoreThreads) paged_score_kernel(const SelectParams p) {
+// CTA (x, row): `rounds` blocks of kScorePages pages of a row.  NT: tiles of 8 heads.
+template <int NT>
+__global__ void __launch_bounds__(kScoreThreads) paged_score_kernel(const SelectParams p,
+                                                                    const int rounds) {
   griddep_wait();
   const int row = blockIdx.y, b = row / p.n_rkv, rk = row % p.n_rkv;
   const int nb = blocks_of(p, b);
-  const int p0 = blockIdx.x * kScorePages;
-  if (p0 >= nb || nb <= p.n_sel) return;  // a row that keeps every page needs no scores
-  __shared__ __align__(16) int8_t qn[16][kD], qp[16][kD];
-  __shared__ float sq[16];
+  int p0 = blockIdx.x * rounds * kScorePages;
+  const int p_end = min(nb, p0 + rounds * kScorePages);
+  if (p0 >= p_end || nb <= p.n_sel) return;  // a row that keeps every page needs no scores
+  __shared__ __align__(16) uint16_t q8[2][NT * 8][kQRow];  // min(q8, 0) and max(q8, 0) as fp16
+  __shared__ float sq[NT * 8];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-
-  // this warp's pages first: their loads overlap the query's
   const int32_t* tab = p.table + (int64_t)b * p.table_stride;
-  uint4 w[kScoreSteps][4];
-  float sp[kScoreSteps];
-#pragma unroll
-  for (int s = 0; s < kScoreSteps; ++s) {
-    const int pg = p0 + (warp * kScoreSteps + s) * 8 + g;
-    const int32_t phys = pg < nb ? tab[pg] : -1;
-    const bool ok = phys >= 0 && phys < p.n_pages;
-    const int64_t at = ok ? (int64_t)phys * p.n_rkv + rk : 0;
-    sp[s] = ok ? p.bound_scale[at] : -1.f;  // negative: no such page
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      w[s][j] = ok ? *reinterpret_cast<const uint4*>(p.bounds + at * 2 * kD + j * 64 + t * 16)
-                   : make_uint4(0, 0, 0, 0);
-  }
 
-  // the G query heads in 8 bits, split by sign; a warp takes heads warp and warp + 8
-  for (int h = warp; h < 16; h += kScoreThreads / 32) {
-    uint32_t neg = 0, pos = 0;
-    float s = 0.f;
+  // this lane's pages: g and g + 8 of the warp's 16
+  int32_t phys[2];
+  uint4 w[2][4];
+  float sp[2];
+  auto locate = [&](int first) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const int pg = first + warp * 16 + s * 8 + g;
+      phys[s] = pg < p_end ? tab[pg] : -1;
+    }
+  };
+  auto load = [&]() {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const bool ok = phys[s] >= 0 && phys[s] < p.n_pages;
+      const int64_t at = ok ? (int64_t)phys[s] * p.n_rkv + rk : 0;
+      sp[s] = ok ? p.bound_scale[at] : -1.f;  // negative: no such page
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        w[s][j] = ok ? *reinterpret_cast<const uint4*>(p.bounds + at * 2 * kD + j * 64 + t * 16)
+                     : make_uint4(0, 0, 0, 0);
+    }
+  };
+  locate(p0);
+
+  // the G query heads in 8-bit steps, split by sign, a warp a head
+  for (int h = warp; h < NT * 8; h += kScoreThreads / 32) {
+    float x[4] = {0.f, 0.f, 0.f, 0.f}, s = 0.f;
     if (h < p.G) {
       const uint2 x2 = *reinterpret_cast<const uint2*>(
           p.q + b * p.q_sb + (int64_t)(p.head[rk] * p.G + h) * kD + lane * 4);
-      const float x[4] = {bf16_lo(x2.x), bf16_hi(x2.x), bf16_lo(x2.y), bf16_hi(x2.y)};
-      bool odd = false;
-      float a = 0.f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        a = fmaxf(a, fabsf(x[i]));
-        odd |= !(fabsf(x[i]) < INFINITY);
-      }
-      a = warp_max(a);
-      s = __any_sync(0xffffffffu, odd) ? 0.f : a * kInv127;
-      if (s > 0.f) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int v = (int)fminf(fmaxf(rintf(x[i] / s), -127.f), 127.f);
-          neg |= (uint32_t)(min(v, 0) & 0xFF) << (8 * i);
-          pos |= (uint32_t)(max(v, 0) & 0xFF) << (8 * i);
-        }
-      }
+      x[0] = bf16_lo(x2.x); x[1] = bf16_hi(x2.x);
+      x[2] = bf16_lo(x2.y); x[3] = bf16_hi(x2.y);
     }
-    *reinterpret_cast<uint32_t*>(&qn[h][lane * 4]) = neg;
-    *reinterpret_cast<uint32_t*>(&qp[h][lane * 4]) = pos;
+    if (h == warp) load();  // the pages' loads overlap the rest of this
+    bool odd = false;
+    float a = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      a = fmaxf(a, fabsf(x[i]));
+      odd |= !(fabsf(x[i]) < INFINITY);
+    }
+    a = warp_max(a);
+    s = __any_sync(0xffffffffu, odd) ? 0.f : a * kInv127;
+    uint16_t neg[4], pos[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float v = s > 0.f ? fminf(fmaxf(rintf(x[i] / s), -127.f), 127.f) : 0.f;
+      neg[i] = __half_as_ushort(__float2half_rn(fminf(v, 0.f)));
+      pos[i] = __half_as_ushort(__float2half_rn(fmaxf(v, 0.f)));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+      *reinterpret_cast<uint32_t*>(&q8[0][h][lane * 4 + i]) = neg[i] | ((uint32_t)neg[i + 1] << 16);
+      *reinterpret_cast<uint32_t*>(&q8[1][h][lane * 4 + i]) = pos[i] | ((uint32_t)pos[i + 1] << 16);
+    }
     if (lane == 0) sq[h] = s;
   }
   __syncthreads();
-
-  // A word i of a thread's 16-byte chunk j pairs with word i of its page's chunk
-  // j: the order of the 256 products is the thread's, the same for A and B
-  int32_t acc[kScoreSteps][4] = {};
+  float sqv[NT][2];  // heads 8 nt + 2 t + {0, 1}
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int8_t(*src)[kD] = j < 2 ? qn : qp;
-    const uint4 lo = *reinterpret_cast<const uint4*>(&src[g][(j & 1) * 64 + t * 16]);
-    const uint4 hi = *reinterpret_cast<const uint4*>(&src[g + 8][(j & 1) * 64 + t * 16]);
-    const uint32_t a0[4] = {lo.x, hi.x, lo.y, hi.y}, a1[4] = {lo.z, hi.z, lo.w, hi.w};
-#pragma unroll
-    for (int s = 0; s < kScoreSteps; ++s) {
-      mma_s8(acc[s], a0, w[s][j].x, w[s][j].y);
-      mma_s8(acc[s], a1, w[s][j].z, w[s][j].w);
-    }
+  for (int nt = 0; nt < NT; ++nt) {
+    sqv[nt][0] = sq[nt * 8 + 2 * t];
+    sqv[nt][1] = sq[nt * 8 + 2 * t + 1];
   }
-  const float q0 = sq[g], q1 = sq[g + 8];
+
+  for (;;) {
+    locate(p0 + kScorePages);  // the next round's table entries arrive during this one
+    // 16 products of 16 dimensions: word u of the lane's chunk j is its four
+    // elements of product 4 j + u, the same dimensions of the query
+    float acc[NT][4] = {};
 #pragma unroll
-  for (int s = 0; s < kScoreSteps; ++s) {
-    float best[2];
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t x0[4] = {w[0][j].x, w[0][j].y, w[0][j].z, w[0][j].w};
+      const uint32_t x1[4] = {w[1][j].x, w[1][j].y, w[1][j].z, w[1][j].w};
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const float spp = __shfl_sync(0xffffffffu, sp[s], 4 * (2 * t + e));
-      float x = -INFINITY;
-      if (spp >= INFINITY) {
-        x = INFINITY;
-      } else if (spp >= 0.f) {  // the product of two scales stays finite
-        if (g < p.G) x = (float)acc[s][e] * fminf(q0 * spp, 3.402823466e38f);
-        if (g + 8 < p.G) x = fmaxf(x, (float)acc[s][2 + e] * fminf(q1 * spp, 3.402823466e38f));
+      for (int u = 0; u < 4; ++u) {
+        uint32_t a0, a1, a2, a3;
+        s8x4_to_f16(x0[u], a0, a2);
+        s8x4_to_f16(x1[u], a1, a3);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const uint2 q = *reinterpret_cast<const uint2*>(
+              &q8[j >> 1][nt * 8 + g][(j & 1) * 64 + t * 16 + u * 4]);
+          mma_f16(acc[nt], a0, a1, a2, a3, q.x, q.y);
+        }
       }
-      x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-      x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-      best[e] = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
     }
-    const int pg = p0 + (warp * kScoreSteps + s) * 8 + 2 * t;
-    if (g < 2) {
-      const int pe = pg + g;
-      if (pe < nb) {
-        const bool forced = pe < p.n_first || pe >= nb - p.n_recent;
-        const float x = forced ? INFINITY : (g ? best[1] : best[0]);
+    const float spv[2] = {sp[0], sp[1]};
+    const bool more = p0 + kScorePages < p_end;
+    if (more) load();
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      float x = -INFINITY;
+      if (spv[s] >= INFINITY) {
+        x = INFINITY;
+      } else if (spv[s] >= 0.f) {  // the product of two scales stays finite
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            if (nt * 8 + 2 * t + c < p.G)
+              x = fmaxf(x, acc[nt][2 * s + c] * fminf(sqv[nt][c] * spv[s], 3.402823466e38f));
+      }
+      x = quad_max(x);
+      const int pe = p0 + warp * 16 + s * 8 + g;
+      if (t == 0 && pe < p_end) {
+        if (pe < p.n_first || pe >= nb - p.n_recent) x = INFINITY;
         p.keys[(int64_t)row * p.width + pe] = score_key(x + 0.f);  // -0 and 0 are one score
       }
     }
+    if (!more) return;
+    p0 += kScorePages;
   }
 }
 
@@ -169,25 +217,43 @@ __device__ __forceinline__ int block_count(int v, int (*sums)[32], int& turn) {
   return all;
 }
 
+constexpr int kTopBins = 2048;
+constexpr int kTopCand = 1024;
+
 // One CTA per row.  E > 0: thread i of warp w holds keys w * 32 E + 32 e + lane;
 // E == 0 (longer rows): the keys are read again from L2 on every pass.
+//
+// The n-th largest key: 2046 equal bins over the row's finite scores, one for
+// those at +inf and one for -inf; the bin that holds it is found by a scan of the
+// counts, and its few keys are ranked against one another.  The bin is a
+// non-decreasing function of the score however its arithmetic rounds, so the
+// result is exact.  A bin of more than 1024 keys (mass ties) is settled bit by
+// bit instead.  Bound by latency: 32 rounds bit by bit took 14 us for 2048 pages and 24
+// for 16384 (traced, with 6 us of events).
 template <int WARPS, int E>
 __global__ void __launch_bounds__(WARPS * 32) paged_topn_kernel(const SelectParams p) {
   griddep_wait();
+  constexpr int kThreads = WARPS * 32;
   __shared__ int sums[2][32];
   __shared__ int base_gt[32], base_eq[32];
+  __shared__ float wlo[32], whi[32];
+  __shared__ int hist[kTopBins];
+  __shared__ __align__(16) uint32_t cand[kTopCand];
+  __shared__ int n_cand, bin_at, bin_above;
+  __shared__ uint32_t cut;
   const int row = blockIdx.x, b = row / p.n_rkv;
   const int nb = blocks_of(p, b), n = p.n_sel;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int32_t* sel = p.sel + (int64_t)row * n;
   if (tid == 0) p.count[row] = min(nb, n);
   if (nb <= n) {
-    for (int i = tid; i < n; i += WARPS * 32) sel[i] = i < nb ? i : -1;
+    for (int i = tid; i < n; i += kThreads) sel[i] = i < nb ? i : -1;
     return;
   }
   const uint32_t* keys = p.keys + (int64_t)row * p.width;
-  const int steps = E > 0 ? E : (nb + WARPS * 32 - 1) / (WARPS * 32);
+  const int steps = E > 0 ? E : (nb + kThreads - 1) / kThreads;
   const int w0 = warp * 32 * steps + lane;  // this thread's first key
+  // a real key is never 0 (-inf maps above it)
   uint32_t kreg[E > 0 ? E : 1];
   if (E > 0) {
 #pragma unroll
@@ -197,15 +263,101 @@ __global__ void __launch_bounds__(WARPS * 32) paged_topn_kernel(const SelectPara
     if (E > 0) return kreg[E > 0 ? e : 0];
     return w0 + 32 * e < nb ? keys[w0 + 32 * e] : 0u;
   };
-  // the largest T with at least n keys >= T; a real key is never 0 (-inf maps above it)
-  uint32_t T = 0;
-  int turn = 0;
-  for (int bit = 31; bit >= 0; --bit) {
-    const uint32_t c = T | (1u << bit);
-    int cnt = 0;
+  for (int i = tid; i < kTopBins; i += kThreads) hist[i] = 0;
+  if (tid == 0) n_cand = 0;
+
+  // range of the finite scores
+  const uint32_t key_pinf = score_key(INFINITY), key_ninf = score_key(-INFINITY);
+  float lo = INFINITY, hi = -INFINITY;
 #pragma unroll
-    for (int e = 0; e < steps; ++e) cnt += key_at(e) >= c;
-    if (block_count<WARPS>(cnt, sums, turn) >= n) T = c;
+  for (int e = 0; e < steps; ++e) {
+    const uint32_t k = key_at(e);
+    if (k > key_ninf && k < key_pinf) {
+      const float x = key_score(k);
+      lo = fminf(lo, x);
+      hi = fmaxf(hi, x);
+    }
+  }
+  lo = -warp_max(-lo);
+  hi = warp_max(hi);
+  if (lane == 0) {
+    wlo[warp] = lo;
+    whi[warp] = hi;
+  }
+  __syncthreads();
+  lo = -warp_max(lane < WARPS ? -wlo[lane] : -INFINITY);
+  hi = warp_max(lane < WARPS ? whi[lane] : -INFINITY);
+  const float half_lo = 0.5f * lo, range = 0.5f * hi - half_lo;  // halves: no overflow
+  const float per = range > 0.f ? fminf((kTopBins - 3) / range, 3.402823466e38f) : 0.f;
+  auto bin_of = [&](uint32_t k) -> int {
+    if (k >= key_pinf) return kTopBins - 1;
+    if (k <= key_ninf) return 0;
+    return 1 + (int)fminf((0.5f * key_score(k) - half_lo) * per, (float)(kTopBins - 3));
+  };
+#pragma unroll
+  for (int e = 0; e < steps; ++e) {
+    const uint32_t k = key_at(e);
+    if (k) atomicAdd(&hist[bin_of(k)], 1);
+  }
+  __syncthreads();
+
+  // the bin that holds the n-th largest: a thread has kTopBins / kThreads bins
+  constexpr int kOwn = kTopBins / kThreads;
+  int own = 0;
+#pragma unroll
+  for (int i = 0; i < kOwn; ++i) own += hist[tid * kOwn + i];
+  int upto = own;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += y;
+  }
+  if (lane == 31) base_gt[warp] = upto;
+  __syncthreads();
+  upto += __reduce_add_sync(0xffffffffu, lane < warp ? base_gt[lane] : 0);
+  int above = nb - upto;  // keys in the bins of higher threads
+  if (above < n && n <= above + own) {
+#pragma unroll
+    for (int i = kOwn - 1; i >= 0; --i) {
+      const int c = hist[tid * kOwn + i];
+      if (above < n && n <= above + c) {
+        bin_at = tid * kOwn + i;
+        bin_above = above;
+      }
+      above += c;
+    }
+  }
+  __syncthreads();
+  const int bin = bin_at, among = n - bin_above, in_bin = hist[bin];
+  uint32_t T = 0;
+  if (in_bin <= kTopCand) {
+#pragma unroll
+    for (int e = 0; e < steps; ++e) {
+      const uint32_t k = key_at(e);
+      if (k && bin_of(k) == bin) cand[atomicAdd(&n_cand, 1)] = k;
+    }
+    __syncthreads();
+    for (int i = tid; i < in_bin; i += kThreads) {
+      const uint32_t k = cand[i];
+      int gt = 0, ge = 0;
+      for (int j = 0; j < in_bin; ++j) {
+        gt += cand[j] > k;
+        ge += cand[j] >= k;
+      }
+      if (gt < among && among <= ge) cut = k;  // equal keys store the same value
+    }
+    __syncthreads();
+    T = cut;
+  } else {
+    int turn = 0;  // the largest T with at least n keys >= T
+    for (int bit = 31; bit >= 0; --bit) {
+      const uint32_t c = T | (1u << bit);
+      int cnt = 0;
+#pragma unroll
+      for (int e = 0; e < steps; ++e) cnt += key_at(e) >= c;
+      if (block_count<WARPS>(cnt, sums, turn) >= n) T = c;
+    }
+    __syncthreads();
   }
   // keys above T all stay; of those equal to T the first ones
   int gt = 0, eq = 0;
@@ -302,9 +454,13 @@ extern "C" rtp_status rtp_paged_block_select(
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (table_width > n_sel) {
     TraceScope tr("paged_score", s);
-    const dim3 grid((table_width + kScorePages - 1) / kScorePages, (unsigned)rows);
-    if ((st = check_cuda(launch_dependent(paged_score_kernel, grid, dim3(kScoreThreads), 0, s,
-                                          p))) != RTP_OK)
+    // one block of pages a CTA while the GPU has room for that (four CTAs an SM),
+    // else several, which reuse the CTA's query and overlap their loads
+    const int64_t blocks = (table_width + kScorePages - 1) / kScorePages;
+    const int rounds = (int)std::min<int64_t>(8, (blocks * rows + 4 * 148 - 1) / (4 * 148));
+    const dim3 grid((unsigned)((blocks + rounds - 1) / rounds), (unsigned)rows);
+    if ((st = check_cuda(launch_dependent(ph.G <= 8 ? paged_score_kernel<1> : paged_score_kernel<2>,
+                                          grid, dim3(kScoreThreads), 0, s, p, rounds))) != RTP_OK)
       return st;
   }
   // the smallest CTA whose registers hold the row
@@ -312,8 +468,8 @@ extern "C" rtp_status rtp_paged_block_select(
   const dim3 grid((unsigned)rows);
   if (table_width <= 8 * 32 * 4)
     return check_cuda(launch_dependent(paged_topn_kernel<8, 4>, grid, dim3(256), 0, s, p));
-  if (table_width <= 32 * 32 * 4)
-    return check_cuda(launch_dependent(paged_topn_kernel<32, 4>, grid, dim3(1024), 0, s, p));
+  if (table_width <= 16 * 32 * 8)
+    return check_cuda(launch_dependent(paged_topn_kernel<16, 8>, grid, dim3(512), 0, s, p));
   if (table_width <= 32 * 32 * 16)
     return check_cuda(launch_dependent(paged_topn_kernel<32, 16>, grid, dim3(1024), 0, s, p));
   return check_cuda(launch_dependent(paged_topn_kernel<32, 0>, grid, dim3(1024), 0, s, p));

@@ -143,6 +143,15 @@ at::Tensor empty(c10::IntArrayRef shape, at::ScalarType type, c10::Device dev) {
   return at::detail::empty_cuda(shape, type, dev, std::nullopt);
 }
 
+// A contiguous tensor on elements from `offset` of buf's storage.
+at::Tensor part(const at::Tensor& buf, int64_t offset, c10::IntArrayRef shape) {
+  at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(buf.storage()),
+                                                          buf.key_set(), buf.dtype());
+  t.unsafeGetTensorImpl()->set_storage_offset(offset);
+  t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
+  return t;
+}
+
 // A workspace that goes back to the allocator, in stream order, when it ends.
 struct Workspace {
   size_t bytes;
@@ -258,11 +267,22 @@ PyObject* plan(PyObject* const* a) {
   }
   const int64_t n_spans = std::min<int64_t>(T, T / ps + 2 * (int64_t)B);
   On on(dev, a[15]);
+  // one allocation for what the caller gave no buffer for, and the workspace
+  const size_t ws_bytes = rtp_paged_workspace_size(RTP_PAGED_PLAN, B, 0, 0, nullptr, 0);
+  auto padded = [](int64_t ints) { return (ints + 63) / 64 * 64; };  // 256-byte places
+  const at::Tensor buf =
+      empty({padded(ws_bytes / 4) + 2 * padded(B) + padded(B + 1) + padded(T) +
+             padded(4 * n_spans) + padded(1)}, at::kInt, dev);
+  int64_t at = padded(ws_bytes / 4);
   at::Tensor out[6];
   auto take = [&](int i, const char* name, std::initializer_list<int64_t> shape,
                   std::initializer_list<int64_t> given) {
-    out[i] = none(a[9 + i]) ? empty(c10::IntArrayRef(shape.begin(), shape.size()), at::kInt, dev)
-                            : tensor(a[9 + i], name, at::kInt, given, dev);
+    if (!none(a[9 + i])) {
+      out[i] = tensor(a[9 + i], name, at::kInt, given, dev);
+      return;
+    }
+    out[i] = part(buf, at, c10::IntArrayRef(shape.begin(), shape.size()));
+    at += padded(out[i].numel());
   };
   take(0, "seq_lens", {B}, {B});
   take(1, "cu_new", {B + 1}, {B + 1});
@@ -276,14 +296,13 @@ PyObject* plan(PyObject* const* a) {
     out[3].zero_().select(1, 0).fill_(-1);
     if (!out[4].is_same(free_count)) out[4].copy_(free_count);
   }
-  Workspace ws(RTP_PAGED_PLAN, B, 0, nullptr, 0);
   check("rtp_paged_plan",
         rtp_paged_plan(B, ps, row, i32(lens), i32(n_new), release, const_cast<int32_t*>(tab.p),
                        tab.stride, tab.width, i32_out(pool),
                        count(pool.size(0), "free_pages: too many"), i32(free_count), T,
                        count(out[3].size(0), "spans: too many"), i32_out(out[0]), i32_out(out[1]),
                        i32_out(out[2]), i32_out(out[3]), i32_out(out[4]), i32_out(out[5]),
-                       ws.data.get(), ws.bytes, raw(on.stream)));
+                       ptr(buf), ws_bytes, raw(on.stream)));
   PyObject* r = PyTuple_New(6);
   if (r == nullptr) throw Set{};
   for (int i = 0; i < 6; ++i) PyTuple_SET_ITEM(r, i, THPVariable_Wrap(out[i]));

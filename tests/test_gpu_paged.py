@@ -463,7 +463,7 @@ def written(kv, x, scale):
 
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
 @pytest.mark.parametrize("layout", ["row", "head"])
-@pytest.mark.parametrize("T,Hkv", [(1, 1), (1, 8), (5, 3), (257, 4)])
+@pytest.mark.parametrize("T,Hkv", [(1, 1), (1, 8), (5, 3), (257, 4), (33, 17), (3, 256), (0, 2)])
 def test_kv_write(kv, layout, T, Hkv):
     g = torch.Generator(device=DEV).manual_seed(T)
     ps, n_pages = 16, 40
@@ -476,7 +476,7 @@ def test_kv_write(kv, layout, T, Hkv):
     k, v = qkv[:, 1], qkv[:, 2]
     sc = torch.rand(2, Hkv, generator=g, device=DEV) * 0.1 + 0.001 if kv == "e4m3" else (None, None)
     slot = torch.randperm(n_pages * ps, generator=g, device=DEV)[:T].to(I32)
-    slot[T // 2] = -1
+    slot[T // 2:T // 2 + 1] = -1
     if T > 4:
         slot[1] = n_pages * ps
         slot[3] = 2 ** 31 - 1
@@ -489,6 +489,34 @@ def test_kv_write(kv, layout, T, Hkv):
                 want[p] = rows[t]
         got = pages.double().cpu().numpy().reshape(n_pages * ps, Hkv, D)
         assert np.array_equal(got, want)
+
+
+def test_kv_write_rounds_the_fp32_quotient():
+    """Scales for which many quotients lie within a unit in the last place of the middle of
+    two e4m3 values, powers of two, subnormal quotients, and scales at the ends of fp32:
+    always the e4m3 value nearest to the fp32 quotient, as torch divides."""
+    g = torch.Generator(device=DEV).manual_seed(5)
+    H = 256
+    x = torch.randn(96, H, D, generator=g, device=DEV, dtype=torch.bfloat16)
+    mid = 2.0 ** torch.randint(-7, 9, (H,), generator=g, device=DEV) * \
+        (1 + (2 * torch.randint(0, 8, (H,), generator=g, device=DEV) + 1) / 16)
+    scale = x[0, :, 0].abs().float() / mid.float()  # x[0] / scale is next to mid
+    scale[:32] = 2.0 ** torch.arange(-16, 16, device=DEV).float()
+    special = [0.0, float("inf"), float("nan"), 1e-45, 1e-38, 2e-38, 3e38, 1.7e38, -0.3, -1e-40,
+               2.0 ** -126, 2.0 ** 127, 2.0 ** -125, 2.0 ** 125]
+    scale[32:32 + len(special)] = torch.tensor(special, device=DEV)
+    x[1:65, :, 0] = x[0, :, 0]  # and its neighbours in bf16
+    x[1:65, :, 0].view(torch.int16).add_(torch.arange(-32, 32, device=DEV, dtype=torch.int16)[:, None])
+    x[65], x[66, :, :4] = 0, torch.tensor([float("inf"), -float("inf"), float("nan"), -0.0])
+    x[67:80] *= 1e-5
+    kp, vp = (torch.zeros(6, 16, H, D, device=DEV).to(torch.float8_e4m3fn) for _ in range(2))
+    rtp_paged_kv_write(x, x, torch.arange(96, device=DEV, dtype=I32), kp, vp, k_scale=scale,
+                       v_scale=scale)
+    want = (x.float() / scale[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn)
+    for got in (kp, vp):
+        a, b = got.view(96, H, D).float(), want.float()
+        assert torch.equal(a.isnan(), b.isnan())
+        assert torch.equal(a.nan_to_num(1.0), b.nan_to_num(1.0))
 
 
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])

@@ -26,6 +26,10 @@
 // whose values fp16 holds exactly), its row sums are taken before that rounding.
 // Beside 8-bit rows q is held in fp16, shifted by a power of two to a maximum in
 // [2^14, 2^15): exact but for elements under 2^-28 of the head's largest.
+#include <cooperative_groups.h>
+
+#include <algorithm>
+
 #include "paged.cuh"
 
 namespace rtp {
@@ -164,16 +168,333 @@ __device__ __forceinline__ void store_final(const PagedAttnParams& p, int b, int
     p.lse[(int64_t)b * p.H + h] = l > 0.f || l != l ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
 
-// NT: tiles of 8 query heads (1 for G <= 8).
+// Tiles [t0, t0 + n_run) of row i of request b by this CTA: leaves each warp's
+// maximum, sum and outputs in shared memory, after a barrier.  NT: tiles of 8 query
+// heads (1 for G <= 8).
+template <bool E4M3, bool SEL, int NT>
+__device__ __forceinline__ void attend_run(const PagedAttnParams& p, AttnSmem<E4M3>& sm, int b,
+                                           int i, int len, int groups, int t0, int n_run) {
+  constexpr int kRow = WarpStages<E4M3>::kRow, kStages = WarpStages<E4M3>::kStages;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const int head = p.head[i];
+  const LocalRange lr = local_range(p, len);
+  const bool local = i >= p.n_rkv;
+  uint8_t* const kst = &sm.w[warp].k[0][0][0];
+  uint8_t* const vst = &sm.w[warp].v[0][0][0];
+  constexpr int kStageBytes = kGroup * kRow;
+  constexpr int kChunks = kRow / 16, kRows = 32 / kChunks;  // 16-byte chunks a row; rows a step
+  const int lr_ = lane / kChunks, lc = lane % kChunks;      // this lane's row of a step and chunk
+  const int64_t k_lane = lr_ * p.kp.row + lc * 16, v_lane = lr_ * p.vp.row + lc * 16;
+
+  // ---- this warp's groups: tile tt of the run is group 4 (t0 + tt) + warp
+  const int32_t* tab = p.table + (int64_t)b * p.table_stride;
+  const int32_t* sl = SEL ? p.sel + ((int64_t)b * p.n_rkv + (local ? 0 : i)) * p.n_sel : nullptr;
+  // first key and physical page of a tile's group; page -1 where there is none
+  auto locate = [&](int tt, int& key0, int& page) {
+    const int gi = kAttnWarps * (t0 + tt) + warp;
+    key0 = 0;
+    page = -1;
+    if (tt >= n_run || gi >= groups) return;
+    if (local) {
+      key0 = (gi < lr.n0 ? gi : lr.w0 + gi - lr.n0) * kGroup;
+    } else if (SEL) {
+      const int per = p.ps_shift - 4;
+      const int lp = sl[gi >> per];
+      if (lp < 0 || lp >= p.width) return;
+      key0 = (lp << p.ps_shift) + (gi & ((1 << per) - 1)) * kGroup;
+    } else {
+      key0 = gi * kGroup;
+    }
+    if (key0 < len) page = tab[key0 >> p.ps_shift];
+  };
+  const uint8_t* const khead = p.kp.ptr + head * p.kp.head + k_lane;
+  const uint8_t* const vhead = p.vp.ptr + head * p.vp.head + v_lane;
+  auto issue = [&](int st, int key0, int page) {
+    uint32_t mask = 0;
+    if (page >= 0 && page < p.n_pages) {
+      const int left = len - key0;
+      mask = left >= kGroup ? 0xFFFFu : (left > 0 ? (1u << left) - 1u : 0u);
+      if (local) {
+        const int below = p.n_sink - key0, from = lr.win_lo - key0;  // j < n_sink or j >= win_lo
+        const uint32_t sink = below >= kGroup ? 0xFFFFu : (below > 0 ? (1u << below) - 1u : 0u);
+        const uint32_t win = from <= 0 ? 0xFFFFu : (from < kGroup ? 0xFFFFu << from : 0u);
+        mask &= sink | win;
+      }
+    }
+    if (lane == 0) sm.mask[warp][st] = mask;
+    if (mask == 0) return;  // nothing to load and nothing read
+    const int row_in = key0 & ((1 << p.ps_shift) - 1);
+    const uint8_t* kb = khead + (int64_t)page * p.kp.page + row_in * p.kp.row;
+    const uint8_t* vb = vhead + (int64_t)page * p.vp.page + row_in * p.vp.row;
+    const uint32_t ks = smem_u32(kst + st * kStageBytes), vs = smem_u32(vst + st * kStageBytes);
+#pragma unroll
+    for (int u = 0; u < kGroup / kRows; ++u) {
+      const int r = u * kRows + lr_;
+      const bool ok = (mask >> r) & 1u;  // other rows become zeros and are not read
+      const int ck = E4M3 ? lc ^ ((r & 1) << 2) : lc ^ (r & 7);
+      const int cv = E4M3 ? lc ^ (((r >> 1) & 3) << 1) : lc ^ (r & 7);
+      cp_async16(ks + r * kRow + ck * 16, kb, ok);
+      cp_async16(vs + r * kRow + cv * 16, vb, ok);
+      kb += kRows * p.kp.row;
+      vb += kRows * p.vp.row;
+    }
+  };
+
+  int key0, page;
+#pragma unroll 1
+  for (int s = 0; s < kStages - 1; ++s) {
+    locate(s, key0, page);
+    if (s < n_run) issue(s, key0, page);
+    cp_async_commit();
+  }
+  locate(kStages - 1, key0, page);
+
+  // ---- query heads nt * 8 + g as product operands (columns; keys are the rows)
+  uint32_t qb[NT][8][2];
+  float ms[NT][2];  // score multipliers of this thread's columns, heads nt * 8 + 2 t + {0, 1}
+  {
+    const uint16_t* q = p.q + b * p.q_sb + (int64_t)head * p.G * kD;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = nt * 8 + g;
+          // 8-bit rows are read 16 bytes a thread: product 4 j + u takes dimensions
+          // 64 j + 16 t + 4 u + {0, 1 | 2, 3}
+          const int d = E4M3 ? 64 * (kk >> 2) + 16 * t + 4 * (kk & 3) + 2 * e
+                             : 16 * kk + 8 * e + 2 * t;
+          qb[nt][kk][e] = r < p.G ? *reinterpret_cast<const uint32_t*>(q + r * kD + d) : 0u;
+        }
+      ms[nt][0] = ms[nt][1] = p.scale_log2;
+      if (E4M3) {
+        float a = 0.f;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            a = fmaxf(a, fmaxf(fabsf(bf16_lo(qb[nt][kk][e])), fabsf(bf16_hi(qb[nt][kk][e]))));
+        a = quad_max(a);
+        int ex = (int)((__float_as_uint(a) >> 23) & 0xFF) - 127;
+        ex = a > 0.f ? max(-100, min(ex, 127)) : 14;
+        const float up = __uint_as_float((uint32_t)(14 - ex + 127) << 23);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            qb[nt][kk][e] = pack_f16x2(bf16_lo(qb[nt][kk][e]) * up, bf16_hi(qb[nt][kk][e]) * up);
+        const float down = p.scale_log2 * (p.k_scale ? p.k_scale[head] : 1.f) *
+                           __uint_as_float((uint32_t)(ex - 14 + 127) << 23);
+        ms[nt][0] = __shfl_sync(0xffffffffu, down, 8 * t);
+        ms[nt][1] = __shfl_sync(0xffffffffu, down, 8 * t + 4);
+      }
+    }
+  }
+
+  // o: 8 tiles of 16 dimensions (rows) x 8 heads (columns)
+  float oacc[NT][8][4];
+  float nref[NT][2], lsum[NT][2];  // kShift - m, and this thread's share of the sum
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+    for (int d = 0; d < 8; ++d)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) oacc[nt][d][e] = 0.f;
+    nref[nt][0] = nref[nt][1] = -kNoRef;
+    lsum[nt][0] = lsum[nt][1] = 0.f;
+  }
+
+  int st = 0, st_in = kStages - 1;  // stage of this tile, and of the one to load
+#pragma unroll 1
+  for (int tt = 0; tt < n_run; ++tt) {
+    cp_async_wait<kStages - 2>();
+    __syncwarp();
+    if (tt + kStages - 1 < n_run) issue(st_in, key0, page);
+    cp_async_commit();
+    locate(tt + kStages, key0, page);  // its table entry arrives during this tile
+    const uint32_t mask = sm.mask[warp][st];
+    const uint8_t* kt = kst + st * kStageBytes;
+    const uint8_t* vt = vst + st * kStageBytes;
+    st = st == kStages - 1 ? 0 : st + 1;
+    st_in = st_in == kStages - 1 ? 0 : st_in + 1;
+    if (mask == 0u) continue;
+
+    // S: 16 keys (rows) x 8 heads; this thread has keys g and g + 8
+    float s[NT][4] = {};
+    if (E4M3) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint8_t* at = kt + g * kRow + ((4 * j + t) ^ ((g & 1) << 2)) * 16;
+        const uint4 w0 = *reinterpret_cast<const uint4*>(at);
+        const uint4 w1 = *reinterpret_cast<const uint4*>(at + 8 * kRow);
+        const uint32_t x0[4] = {w0.x, w0.y, w0.z, w0.w}, x1[4] = {w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const uint32_t a[4] = {
+              e4m3x2_to_f16x2((uint16_t)x0[u]), e4m3x2_to_f16x2((uint16_t)x1[u]),
+              e4m3x2_to_f16x2((uint16_t)(x0[u] >> 16)), e4m3x2_to_f16x2((uint16_t)(x1[u] >> 16))};
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma16816_f16(s[nt], a, qb[nt][4 * j + u][0], qb[nt][4 * j + u][1]);
+        }
+      }
+    } else {
+      const int r = lane & 15;
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk) {
+        uint32_t a[4];
+        ldmatrix_x4(a, smem_u32(kt + r * kRow + (((2 * kk + (lane >> 4)) ^ (r & 7)) << 4)));
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          mma16816(s[nt], a, qb[nt][kk][0], qb[nt][kk][1], s[nt]);
+      }
+    }
+    if (mask != 0xFFFFu) {
+      const bool ok0 = (mask >> g) & 1u, ok1 = (mask >> (g + 8)) & 1u;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        // the multipliers are positive
+        if (!ok0) s[nt][0] = s[nt][1] = -INFINITY;
+        if (!ok1) s[nt][2] = s[nt][3] = -INFINITY;
+      }
+    }
+    float y[NT][4];
+    bool grow = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        y[nt][e] = fmaf(s[nt][e], ms[nt][e & 1], nref[nt][e & 1]);
+        grow |= y[nt][e] > kGrow + kShift<E4M3>;
+      }
+    if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float m = fmaxf(s[nt][c], s[nt][2 + c]) * ms[nt][c];
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+          const float to = fminf(nref[nt][c], kShift<E4M3> - m);
+          const float alpha = ex2(to - nref[nt][c]);
+          nref[nt][c] = to;
+          lsum[nt][c] *= alpha;
+#pragma unroll
+          for (int d = 0; d < 8; ++d) {
+            oacc[nt][d][c] *= alpha;
+            oacc[nt][d][2 + c] *= alpha;
+          }
+          y[nt][c] = fmaf(s[nt][c], ms[nt][c], to);
+          y[nt][2 + c] = fmaf(s[nt][2 + c], ms[nt][c], to);
+        }
+    }
+    uint32_t pb[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float pr[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) pr[e] = ex2(y[nt][e]);
+      lsum[nt][0] += pr[0] + pr[2];
+      lsum[nt][1] += pr[1] + pr[3];
+      pb[nt][0] = transpose8x8(E4M3 ? pack_f16x2(pr[0], pr[1]) : pack_bf16x2(pr[0], pr[1]));
+      pb[nt][1] = transpose8x8(E4M3 ? pack_f16x2(pr[2], pr[3]) : pack_bf16x2(pr[2], pr[3]));
+    }
+    if (E4M3) {
+      // the thread's keys 2t, 2t+1, 2t+8, 2t+9, dimensions 16 g .. 16 g + 15:
+      // product d takes dimensions 16 n + 2 d (its row n) and 16 n + 2 d + 1 (n + 8)
+      uint4 w[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        w[u] = *reinterpret_cast<const uint4*>(vt + (2 * t + (u & 1) + 8 * (u >> 1)) * kRow +
+                                               ((g ^ (t << 1)) << 4));
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t x[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          x[u] = c == 0 ? w[u].x : c == 1 ? w[u].y : c == 2 ? w[u].z : w[u].w;
+#pragma unroll
+        for (int hlf = 0; hlf < 2; ++hlf) {
+          const uint32_t sel = hlf ? 0x7362u : 0x5140u;
+          const uint32_t lo = __byte_perm(x[0], x[1], sel), hi = __byte_perm(x[2], x[3], sel);
+          const uint32_t a[4] = {
+              e4m3x2_to_f16x2((uint16_t)lo), e4m3x2_to_f16x2((uint16_t)(lo >> 16)),
+              e4m3x2_to_f16x2((uint16_t)hi), e4m3x2_to_f16x2((uint16_t)(hi >> 16))};
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma16816_f16(oacc[nt][2 * c + hlf], a, pb[nt][0], pb[nt][1]);
+        }
+      }
+    } else {
+      const int r = (lane & 7) + 8 * (lane >> 4);  // matrices: keys lo, dims lo | dims hi; keys hi ...
+#pragma unroll
+      for (int d = 0; d < 8; ++d) {
+        uint32_t a[4];
+        ldmatrix_x4_trans(
+            a, smem_u32(vt + r * kRow + (((2 * d + ((lane >> 3) & 1)) ^ (r & 7)) << 4)));
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          mma16816(oacc[nt][d], a, pb[nt][0], pb[nt][1], oacc[nt][d]);
+      }
+    }
+  }
+  cp_async_wait<0>();
+  __syncwarp();
+
+  // ---- join the four warps; each leaves its rows in its own (now idle) stages
+  float* wo = reinterpret_cast<float*>(kst);
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      float l = lsum[nt][c];
+      l += __shfl_xor_sync(0xffffffffu, l, 4);
+      l += __shfl_xor_sync(0xffffffffu, l, 8);
+      l += __shfl_xor_sync(0xffffffffu, l, 16);
+      const int r = nt * 8 + 2 * t + c;
+      if (r < p.G) {
+        if (g == 0) {
+          sm.wm[warp][r] = nref[nt][c] == -kNoRef ? -INFINITY : kShift<E4M3> - nref[nt][c];
+          sm.wl[warp][r] = l;
+        }
+#pragma unroll
+        for (int d = 0; d < 8; ++d) {
+          wo[r * kD + (E4M3 ? 16 * g + 2 * d : 16 * d + g)] = oacc[nt][d][c];
+          wo[r * kD + (E4M3 ? 16 * g + 2 * d + 1 : 16 * d + g + 8)] = oacc[nt][d][2 + c];
+        }
+      }
+    }
+  __syncthreads();
+}
+
+// A finished run's result for one query head and dimension: the warps' joined.
+template <bool E4M3>
+__device__ __forceinline__ void join_warps(const AttnSmem<E4M3>& sm, int r, int d, float& M,
+                                           float& l, float& o) {
+  M = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < kAttnWarps; ++w) M = fmaxf(M, sm.wm[w][r]);
+  o = l = 0.f;
+#pragma unroll
+  for (int w = 0; w < kAttnWarps; ++w) {
+    // a warp that saw no key has l = 0 and o = 0; a NaN score leaves NaN in l and o
+    const float f = ex2(sm.wm[w][r] - (M == -INFINITY ? 0.f : M) - kShift<E4M3>);
+    const float fw = sm.wm[w][r] == -INFINITY && sm.wl[w][r] == sm.wl[w][r] ? 0.f : f;
+    o += fw * reinterpret_cast<const float*>(&sm.w[w].k[0][0][0])[r * kD + d];
+    l += fw * sm.wl[w][r];
+  }
+}
+
 template <bool E4M3, bool SEL, int NT>
 __global__ void __launch_bounds__(kAttnThreads, WarpStages<E4M3>::kCtasPerSm)
     paged_attn_kernel(const PagedAttnParams p) {
   griddep_wait();
   extern __shared__ __align__(128) unsigned char smem_raw[];
   AttnSmem<E4M3>& sm = *reinterpret_cast<AttnSmem<E4M3>*>(smem_raw);
-  constexpr int kRow = WarpStages<E4M3>::kRow, kStages = WarpStages<E4M3>::kStages;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int g = lane >> 2, t = lane & 3;
 
   // ---- this CTA's run of tiles
   auto scan = [&](int64_t v, int64_t& all) {  // exclusive over the CTA
@@ -230,13 +551,6 @@ __global__ void __launch_bounds__(kAttnThreads, WarpStages<E4M3>::kCtasPerSm)
   int64_t row0 = sm.first;  // first tile of row (b, i)
   const int64_t start = pos;
 
-  uint8_t* const kst = &sm.w[warp].k[0][0][0];
-  uint8_t* const vst = &sm.w[warp].v[0][0][0];
-  constexpr int kStageBytes = kGroup * kRow;
-  constexpr int kChunks = kRow / 16, kRows = 32 / kChunks;  // 16-byte chunks a row; rows a step
-  const int lr_ = lane / kChunks, lc = lane % kChunks;      // this lane's row of a step and chunk
-  const int64_t k_lane = lr_ * p.kp.row + lc * 16, v_lane = lr_ * p.vp.row + lc * 16;
-
   for (;;) {
     // ---- the row that holds tile `pos`
     int groups = row_groups<SEL>(p, b, i, len);
@@ -251,307 +565,14 @@ __global__ void __launch_bounds__(kAttnThreads, WarpStages<E4M3>::kCtasPerSm)
     const int head = p.head[i];
     const int t0 = (int)(pos - row0), tiles = tiles_of(groups);
     const int t1 = (int)min((int64_t)tiles, t0 + (end - pos));
-    const LocalRange lr = local_range(p, len);
-    const bool local = i >= p.n_rkv;
     if (t0 == 0 && tid == 0) p.meta[1 + (int64_t)b * p.Hkv + i] = pos;
 
-    // ---- this warp's groups: tile tt of the run is group 4 (t0 + tt) + warp
-    const int n_run = t1 - t0;
-    const int32_t* tab = p.table + (int64_t)b * p.table_stride;
-    const int32_t* sl = SEL ? p.sel + ((int64_t)b * p.n_rkv + (local ? 0 : i)) * p.n_sel : nullptr;
-    // first key and physical page of a tile's group; page -1 where there is none
-    auto locate = [&](int tt, int& key0, int& page) {
-      const int gi = kAttnWarps * (t0 + tt) + warp;
-      key0 = 0;
-      page = -1;
-      if (tt >= n_run || gi >= groups) return;
-      if (local) {
-        key0 = (gi < lr.n0 ? gi : lr.w0 + gi - lr.n0) * kGroup;
-      } else if (SEL) {
-        const int per = p.ps_shift - 4;
-        const int lp = sl[gi >> per];
-        if (lp < 0 || lp >= p.width) return;
-        key0 = (lp << p.ps_shift) + (gi & ((1 << per) - 1)) * kGroup;
-      } else {
-        key0 = gi * kGroup;
-      }
-      if (key0 < len) page = tab[key0 >> p.ps_shift];
-    };
-    const uint8_t* const khead = p.kp.ptr + head * p.kp.head + k_lane;
-    const uint8_t* const vhead = p.vp.ptr + head * p.vp.head + v_lane;
-    auto issue = [&](int st, int key0, int page) {
-      uint32_t mask = 0;
-      if (page >= 0 && page < p.n_pages) {
-        const int left = len - key0;
-        mask = left >= kGroup ? 0xFFFFu : (left > 0 ? (1u << left) - 1u : 0u);
-        if (local) {
-          const int below = p.n_sink - key0, from = lr.win_lo - key0;  // j < n_sink or j >= win_lo
-          const uint32_t sink = below >= kGroup ? 0xFFFFu : (below > 0 ? (1u << below) - 1u : 0u);
-          const uint32_t win = from <= 0 ? 0xFFFFu : (from < kGroup ? 0xFFFFu << from : 0u);
-          mask &= sink | win;
-        }
-      }
-      if (lane == 0) sm.mask[warp][st] = mask;
-      if (mask == 0) return;  // nothing to load and nothing read
-      const int row_in = key0 & ((1 << p.ps_shift) - 1);
-      const uint8_t* kb = khead + (int64_t)page * p.kp.page + row_in * p.kp.row;
-      const uint8_t* vb = vhead + (int64_t)page * p.vp.page + row_in * p.vp.row;
-      const uint32_t ks = smem_u32(kst + st * kStageBytes), vs = smem_u32(vst + st * kStageBytes);
-#pragma unroll
-      for (int u = 0; u < kGroup / kRows; ++u) {
-        const int r = u * kRows + lr_;
-        const bool ok = (mask >> r) & 1u;  // other rows become zeros and are not read
-        const int ck = E4M3 ? lc ^ ((r & 1) << 2) : lc ^ (r & 7);
-        const int cv = E4M3 ? lc ^ (((r >> 1) & 3) << 1) : lc ^ (r & 7);
-        cp_async16(ks + r * kRow + ck * 16, kb, ok);
-        cp_async16(vs + r * kRow + cv * 16, vb, ok);
-        kb += kRows * p.kp.row;
-        vb += kRows * p.vp.row;
-      }
-    };
-
-    int key0, page;
-#pragma unroll 1
-    for (int s = 0; s < kStages - 1; ++s) {
-      locate(s, key0, page);
-      if (s < n_run) issue(s, key0, page);
-      cp_async_commit();
-    }
-    locate(kStages - 1, key0, page);
-
-    // ---- query heads nt * 8 + g as product operands (columns; keys are the rows)
-    uint32_t qb[NT][8][2];
-    float ms[NT][2];  // score multipliers of this thread's columns, heads nt * 8 + 2 t + {0, 1}
-    {
-      const uint16_t* q = p.q + b * p.q_sb + (int64_t)head * p.G * kD;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int r = nt * 8 + g;
-            // 8-bit rows are read 16 bytes a thread: product 4 j + u takes dimensions
-            // 64 j + 16 t + 4 u + {0, 1 | 2, 3}
-            const int d = E4M3 ? 64 * (kk >> 2) + 16 * t + 4 * (kk & 3) + 2 * e
-                               : 16 * kk + 8 * e + 2 * t;
-            qb[nt][kk][e] = r < p.G ? *reinterpret_cast<const uint32_t*>(q + r * kD + d) : 0u;
-          }
-        ms[nt][0] = ms[nt][1] = p.scale_log2;
-        if (E4M3) {
-          float a = 0.f;
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-              a = fmaxf(a, fmaxf(fabsf(bf16_lo(qb[nt][kk][e])), fabsf(bf16_hi(qb[nt][kk][e]))));
-          a = quad_max(a);
-          int ex = (int)((__float_as_uint(a) >> 23) & 0xFF) - 127;
-          ex = a > 0.f ? max(-100, min(ex, 127)) : 14;
-          const float up = __uint_as_float((uint32_t)(14 - ex + 127) << 23);
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-              qb[nt][kk][e] = pack_f16x2(bf16_lo(qb[nt][kk][e]) * up, bf16_hi(qb[nt][kk][e]) * up);
-          const float down = p.scale_log2 * (p.k_scale ? p.k_scale[head] : 1.f) *
-                             __uint_as_float((uint32_t)(ex - 14 + 127) << 23);
-          ms[nt][0] = __shfl_sync(0xffffffffu, down, 8 * t);
-          ms[nt][1] = __shfl_sync(0xffffffffu, down, 8 * t + 4);
-        }
-      }
-    }
-
-    // o: 8 tiles of 16 dimensions (rows) x 8 heads (columns)
-    float oacc[NT][8][4];
-    float nref[NT][2], lsum[NT][2];  // kShift - m, and this thread's share of the sum
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-      for (int d = 0; d < 8; ++d)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) oacc[nt][d][e] = 0.f;
-      nref[nt][0] = nref[nt][1] = -kNoRef;
-      lsum[nt][0] = lsum[nt][1] = 0.f;
-    }
-
-    int st = 0, st_in = kStages - 1;  // stage of this tile, and of the one to load
-#pragma unroll 1
-    for (int tt = 0; tt < n_run; ++tt) {
-      cp_async_wait<kStages - 2>();
-      __syncwarp();
-      if (tt + kStages - 1 < n_run) issue(st_in, key0, page);
-      cp_async_commit();
-      locate(tt + kStages, key0, page);  // its table entry arrives during this tile
-      const uint32_t mask = sm.mask[warp][st];
-      const uint8_t* kt = kst + st * kStageBytes;
-      const uint8_t* vt = vst + st * kStageBytes;
-      st = st == kStages - 1 ? 0 : st + 1;
-      st_in = st_in == kStages - 1 ? 0 : st_in + 1;
-      if (mask == 0u) continue;
-
-      // S: 16 keys (rows) x 8 heads; this thread has keys g and g + 8
-      float s[NT][4] = {};
-      if (E4M3) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const uint8_t* at = kt + g * kRow + ((4 * j + t) ^ ((g & 1) << 2)) * 16;
-          const uint4 w0 = *reinterpret_cast<const uint4*>(at);
-          const uint4 w1 = *reinterpret_cast<const uint4*>(at + 8 * kRow);
-          const uint32_t x0[4] = {w0.x, w0.y, w0.z, w0.w}, x1[4] = {w1.x, w1.y, w1.z, w1.w};
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const uint32_t a[4] = {
-                e4m3x2_to_f16x2((uint16_t)x0[u]), e4m3x2_to_f16x2((uint16_t)x1[u]),
-                e4m3x2_to_f16x2((uint16_t)(x0[u] >> 16)), e4m3x2_to_f16x2((uint16_t)(x1[u] >> 16))};
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma16816_f16(s[nt], a, qb[nt][4 * j + u][0], qb[nt][4 * j + u][1]);
-          }
-        }
-      } else {
-        const int r = lane & 15;
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          uint32_t a[4];
-          ldmatrix_x4(a, smem_u32(kt + r * kRow + (((2 * kk + (lane >> 4)) ^ (r & 7)) << 4)));
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            mma16816(s[nt], a, qb[nt][kk][0], qb[nt][kk][1], s[nt]);
-        }
-      }
-      if (mask != 0xFFFFu) {
-        const bool ok0 = (mask >> g) & 1u, ok1 = (mask >> (g + 8)) & 1u;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          // the multipliers are positive
-          if (!ok0) s[nt][0] = s[nt][1] = -INFINITY;
-          if (!ok1) s[nt][2] = s[nt][3] = -INFINITY;
-        }
-      }
-      float y[NT][4];
-      bool grow = false;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          y[nt][e] = fmaf(s[nt][e], ms[nt][e & 1], nref[nt][e & 1]);
-          grow |= y[nt][e] > kGrow + kShift<E4M3>;
-        }
-      if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float m = fmaxf(s[nt][c], s[nt][2 + c]) * ms[nt][c];
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-            const float to = fminf(nref[nt][c], kShift<E4M3> - m);
-            const float alpha = ex2(to - nref[nt][c]);
-            nref[nt][c] = to;
-            lsum[nt][c] *= alpha;
-#pragma unroll
-            for (int d = 0; d < 8; ++d) {
-              oacc[nt][d][c] *= alpha;
-              oacc[nt][d][2 + c] *= alpha;
-            }
-            y[nt][c] = fmaf(s[nt][c], ms[nt][c], to);
-            y[nt][2 + c] = fmaf(s[nt][2 + c], ms[nt][c], to);
-          }
-      }
-      uint32_t pb[NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float pr[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) pr[e] = ex2(y[nt][e]);
-        lsum[nt][0] += pr[0] + pr[2];
-        lsum[nt][1] += pr[1] + pr[3];
-        pb[nt][0] = transpose8x8(E4M3 ? pack_f16x2(pr[0], pr[1]) : pack_bf16x2(pr[0], pr[1]));
-        pb[nt][1] = transpose8x8(E4M3 ? pack_f16x2(pr[2], pr[3]) : pack_bf16x2(pr[2], pr[3]));
-      }
-      if (E4M3) {
-        // the thread's keys 2t, 2t+1, 2t+8, 2t+9, dimensions 16 g .. 16 g + 15:
-        // product d takes dimensions 16 n + 2 d (its row n) and 16 n + 2 d + 1 (n + 8)
-        uint4 w[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-          w[u] = *reinterpret_cast<const uint4*>(vt + (2 * t + (u & 1) + 8 * (u >> 1)) * kRow +
-                                                 ((g ^ (t << 1)) << 4));
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t x[4];
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            x[u] = c == 0 ? w[u].x : c == 1 ? w[u].y : c == 2 ? w[u].z : w[u].w;
-#pragma unroll
-          for (int hlf = 0; hlf < 2; ++hlf) {
-            const uint32_t sel = hlf ? 0x7362u : 0x5140u;
-            const uint32_t lo = __byte_perm(x[0], x[1], sel), hi = __byte_perm(x[2], x[3], sel);
-            const uint32_t a[4] = {
-                e4m3x2_to_f16x2((uint16_t)lo), e4m3x2_to_f16x2((uint16_t)(lo >> 16)),
-                e4m3x2_to_f16x2((uint16_t)hi), e4m3x2_to_f16x2((uint16_t)(hi >> 16))};
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma16816_f16(oacc[nt][2 * c + hlf], a, pb[nt][0], pb[nt][1]);
-          }
-        }
-      } else {
-        const int r = (lane & 7) + 8 * (lane >> 4);  // matrices: keys lo, dims lo | dims hi; keys hi ...
-#pragma unroll
-        for (int d = 0; d < 8; ++d) {
-          uint32_t a[4];
-          ldmatrix_x4_trans(
-              a, smem_u32(vt + r * kRow + (((2 * d + ((lane >> 3) & 1)) ^ (r & 7)) << 4)));
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            mma16816(oacc[nt][d], a, pb[nt][0], pb[nt][1], oacc[nt][d]);
-        }
-      }
-    }
-    cp_async_wait<0>();
-    __syncwarp();
-
-    // ---- join the four warps; each leaves its rows in its own (now idle) stages
-    float* wo = reinterpret_cast<float*>(kst);
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float l = lsum[nt][c];
-        l += __shfl_xor_sync(0xffffffffu, l, 4);
-        l += __shfl_xor_sync(0xffffffffu, l, 8);
-        l += __shfl_xor_sync(0xffffffffu, l, 16);
-        const int r = nt * 8 + 2 * t + c;
-        if (r < p.G) {
-          if (g == 0) {
-            sm.wm[warp][r] = nref[nt][c] == -kNoRef ? -INFINITY : kShift<E4M3> - nref[nt][c];
-            sm.wl[warp][r] = l;
-          }
-#pragma unroll
-          for (int d = 0; d < 8; ++d) {
-            wo[r * kD + (E4M3 ? 16 * g + 2 * d : 16 * d + g)] = oacc[nt][d][c];
-            wo[r * kD + (E4M3 ? 16 * g + 2 * d + 1 : 16 * d + g + 8)] = oacc[nt][d][2 + c];
-          }
-        }
-      }
-    __syncthreads();
+    attend_run<E4M3, SEL, NT>(p, sm, b, i, len, groups, t0, t1 - t0);
     const bool whole = t0 == 0 && t1 == tiles;
     float* part = p.part + ((int64_t)blockIdx.x * 2 + (pos == start ? 0 : 1)) * p.G * kPartRow;
     for (int r = 0; r < p.G; ++r) {
-      float M = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kAttnWarps; ++w) M = fmaxf(M, sm.wm[w][r]);
-      float o = 0.f, l = 0.f;
-#pragma unroll
-      for (int w = 0; w < kAttnWarps; ++w) {
-        // a warp that saw no key has l = 0 and o = 0; a NaN score leaves NaN in l and o
-        const float f = ex2(sm.wm[w][r] - (M == -INFINITY ? 0.f : M) - kShift<E4M3>);
-        const float fw = sm.wm[w][r] == -INFINITY && sm.wl[w][r] == sm.wl[w][r] ? 0.f : f;
-        o += fw * reinterpret_cast<const float*>(&sm.w[w].k[0][0][0])[r * kD + tid];
-        l += fw * sm.wl[w][r];
-      }
+      float M, l, o;
+      join_warps<E4M3>(sm, r, tid, M, l, o);
       if (whole) {
         store_final(p, b, head, r, tid, M, l, o);
       } else {
@@ -562,10 +583,65 @@ __global__ void __launch_bounds__(kAttnThreads, WarpStages<E4M3>::kCtasPerSm)
         }
       }
     }
-    pos += n_run;
+    pos += t1 - t0;
     if (pos >= end) return;
     __syncthreads();
   }
+}
+
+// The same for few and short rows, without a second kernel: a cluster of eight
+// CTAs takes a row, each an equal run of its tiles, and joins them through
+// distributed shared memory in rank order.
+constexpr int kCluster = 8;
+
+template <bool E4M3, bool SEL, int NT>
+__global__ void __cluster_dims__(kCluster, 1, 1)
+    __launch_bounds__(kAttnThreads, WarpStages<E4M3>::kCtasPerSm)
+        paged_attn_short_kernel(const PagedAttnParams p) {
+  griddep_wait();
+  namespace cg = cooperative_groups;
+  extern __shared__ __align__(128) unsigned char smem_raw[];
+  AttnSmem<E4M3>& sm = *reinterpret_cast<AttnSmem<E4M3>*>(smem_raw);
+  __shared__ __align__(16) float part[16][kPartRow];  // m, l, pad, o of this CTA's run
+  const cg::cluster_group cluster = cg::this_cluster();
+  const int row = blockIdx.x / kCluster, rank = blockIdx.x % kCluster;
+  const int b = row / p.Hkv, i = row % p.Hkv, tid = threadIdx.x;
+  const int len = paged_len(p, b), groups = row_groups<SEL>(p, b, i, len);
+  const int tiles = tiles_of(groups);
+  const int t0 = (int)((int64_t)tiles * rank / kCluster);
+  attend_run<E4M3, SEL, NT>(p, sm, b, i, len, groups, t0,
+                            (int)((int64_t)tiles * (rank + 1) / kCluster) - t0);
+  for (int r = 0; r < p.G; ++r) {
+    float M, l, o;
+    join_warps<E4M3>(sm, r, tid, M, l, o);
+    part[r][4 + tid] = o;
+    if (tid == 0) {
+      part[r][0] = M;
+      part[r][1] = l;
+    }
+  }
+  cluster.sync();
+  for (int r = rank; r < p.G; r += kCluster) {
+    float m[kCluster], l[kCluster], o[kCluster], M = -INFINITY;
+#pragma unroll
+    for (int c = 0; c < kCluster; ++c) {
+      const float* x = cluster.map_shared_rank(&part[r][0], c);
+      m[c] = x[0];
+      l[c] = x[1];
+      o[c] = x[4 + tid];
+      M = fmaxf(M, m[c]);
+    }
+    const float m0 = M == -INFINITY ? 0.f : M;
+    float ls = 0.f, os = 0.f;
+#pragma unroll
+    for (int c = 0; c < kCluster; ++c) {
+      const float f = m[c] == -INFINITY && l[c] == l[c] ? 0.f : ex2(m[c] - m0);
+      ls += f * l[c];
+      os += f * o[c];
+    }
+    store_final(p, b, p.head[i], r, tid, M, ls, os);
+  }
+  cluster.sync();  // no CTA leaves while another reads its part
 }
 
 // Joins a row's partials, in CTA order, one CTA per (request, kv head, query
@@ -624,20 +700,25 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const PagedAttnParams p
 constexpr int kSms = 148;
 constexpr int kMaxAttnCtas = 3 * kSms;
 
+// Clusters of eight suit rows of up to 128 tiles (in a request as long as its
+// table allows), while all clusters are on the GPU at once.
+constexpr int kShortTiles = 128;
+
 template <bool E4M3, bool SEL, int NT>
-rtp_status launch(const PagedAttnParams& p, cudaStream_t s) {
+rtp_status launch(const PagedAttnParams& p, int max_tiles, cudaStream_t s) {
   const size_t smem = sizeof(AttnSmem<E4M3>);
   constexpr int ctas = WarpStages<E4M3>::kCtasPerSm * kSms;
   static_assert(ctas <= kMaxAttnCtas, "the workspace holds every CTA's partials");
-  auto* kernel = paged_attn_kernel<E4M3, SEL, NT>;
+  const bool brief = max_tiles <= kShortTiles && (int64_t)p.B * p.Hkv * kCluster <= ctas;
+  auto* kernel = brief ? paged_attn_short_kernel<E4M3, SEL, NT> : paged_attn_kernel<E4M3, SEL, NT>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
       cudaSuccess)
     return RTP_ERR_CUDA;
   rtp_status st;
   {
     TraceScope tr("paged_attn", s);
-    if ((st = check_cuda(launch_dependent(kernel, dim3(ctas), dim3(kAttnThreads), smem, s, p))) !=
-        RTP_OK)
+    if ((st = check_cuda(launch_dependent(kernel, dim3(brief ? p.B * p.Hkv * kCluster : ctas),
+                                          dim3(kAttnThreads), smem, s, p))) != RTP_OK || brief)
       return st;
   }
   TraceScope tr("paged_join", s);
@@ -646,8 +727,8 @@ rtp_status launch(const PagedAttnParams& p, cudaStream_t s) {
 }
 
 template <bool E4M3, bool SEL>
-rtp_status launch(const PagedAttnParams& p, cudaStream_t s) {
-  return p.G <= 8 ? launch<E4M3, SEL, 1>(p, s) : launch<E4M3, SEL, 2>(p, s);
+rtp_status launch(const PagedAttnParams& p, int max_tiles, cudaStream_t s) {
+  return p.G <= 8 ? launch<E4M3, SEL, 1>(p, max_tiles, s) : launch<E4M3, SEL, 2>(p, max_tiles, s);
 }
 
 struct AttnWs {
@@ -741,7 +822,13 @@ extern "C" rtp_status rtp_paged_attn_decode(
   p.n_sel = n_sel;
   memcpy(p.head, ph.head, sizeof(p.head));
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  // the longest row's tiles, as far as the host can tell
+  const int64_t most = (int64_t)table_width * k_pages.page_size;
+  int64_t keys = 0;
+  if (ph.n_rkv > 0) keys = sel ? (int64_t)n_sel * k_pages.page_size : most;
+  if (ph.n_rkv < Hkv) keys = std::max(keys, std::min(most, (int64_t)window + n_sink + 3 * kGroup));
+  const int max_tiles = (int)((keys + kAttnWarps * kGroup - 1) / (kAttnWarps * kGroup));
   if (k_pages.type == RTP_KV_E4M3)
-    return sel ? launch<true, true>(p, s) : launch<true, false>(p, s);
-  return sel ? launch<false, true>(p, s) : launch<false, false>(p, s);
+    return sel ? launch<true, true>(p, max_tiles, s) : launch<true, false>(p, max_tiles, s);
+  return sel ? launch<false, true>(p, max_tiles, s) : launch<false, false>(p, max_tiles, s);
 }

@@ -149,7 +149,6 @@ struct WarpStages {
 template <bool E4M3>
 struct AttnSmem {
   WarpStages<E4M3> w[kAttnWarps];  // a finished run's partial outputs reuse each warp's stages
-  uint32_t mask[kAttnWarps][8];    // per stage: bit r = key r of the group counts
   float wm[kAttnWarps][16], wl[kAttnWarps][16];
   int64_t sums[kAttnWarps], first;
   int req;
@@ -190,12 +189,15 @@ __device__ __forceinline__ void attend_run(const PagedAttnParams& p, AttnSmem<E4
   // ---- this warp's groups: tile tt of the run is group 4 (t0 + tt) + warp
   const int32_t* tab = p.table + (int64_t)b * p.table_stride;
   const int32_t* sl = SEL ? p.sel + ((int64_t)b * p.n_rkv + (local ? 0 : i)) * p.n_sel : nullptr;
-  // first key and physical page of a tile's group; page -1 where there is none
-  auto locate = [&](int tt, int& key0, int& page) {
-    const int gi = kAttnWarps * (t0 + tt) + warp;
-    key0 = 0;
+  // Each lane looks one tile's group up, 32 tiles at once: its physical page (-1
+  // where there is none), and its first row in the page with the keys that count
+  // (bit r of the low half: key r of the group).
+  auto locate = [&](int first, int& page, uint32_t& rows) {
+    const int tt = first + lane, gi = kAttnWarps * (t0 + tt) + warp;
     page = -1;
+    rows = 0;
     if (tt >= n_run || gi >= groups) return;
+    int key0 = gi * kGroup;
     if (local) {
       key0 = (gi < lr.n0 ? gi : lr.w0 + gi - lr.n0) * kGroup;
     } else if (SEL) {
@@ -203,28 +205,36 @@ __device__ __forceinline__ void attend_run(const PagedAttnParams& p, AttnSmem<E4
       const int lp = sl[gi >> per];
       if (lp < 0 || lp >= p.width) return;
       key0 = (lp << p.ps_shift) + (gi & ((1 << per) - 1)) * kGroup;
-    } else {
-      key0 = gi * kGroup;
     }
-    if (key0 < len) page = tab[key0 >> p.ps_shift];
+    if (key0 >= len) return;
+    page = tab[key0 >> p.ps_shift];
+    uint32_t mask = len - key0 >= kGroup ? 0xFFFFu : (1u << (len - key0)) - 1u;
+    if (local) {
+      const int below = p.n_sink - key0, from = lr.win_lo - key0;  // j < n_sink or j >= win_lo
+      const uint32_t sink = below >= kGroup ? 0xFFFFu : (below > 0 ? (1u << below) - 1u : 0u);
+      const uint32_t win = from <= 0 ? 0xFFFFu : (from < kGroup ? 0xFFFFu << from : 0u);
+      mask &= sink | win;
+    }
+    rows = ((uint32_t)(key0 & ((1 << p.ps_shift) - 1)) << 16) | mask;
   };
   const uint8_t* const khead = p.kp.ptr + head * p.kp.head + k_lane;
   const uint8_t* const vhead = p.vp.ptr + head * p.vp.head + v_lane;
-  auto issue = [&](int st, int key0, int page) {
-    uint32_t mask = 0;
-    if (page >= 0 && page < p.n_pages) {
-      const int left = len - key0;
-      mask = left >= kGroup ? 0xFFFFu : (left > 0 ? (1u << left) - 1u : 0u);
-      if (local) {
-        const int below = p.n_sink - key0, from = lr.win_lo - key0;  // j < n_sink or j >= win_lo
-        const uint32_t sink = below >= kGroup ? 0xFFFFu : (below > 0 ? (1u << below) - 1u : 0u);
-        const uint32_t win = from <= 0 ? 0xFFFFu : (from < kGroup ? 0xFFFFu << from : 0u);
-        mask &= sink | win;
-      }
+  int page_now, page_next = -1;
+  uint32_t rows_now, rows_next = 0;
+  locate(0, page_now, rows_now);
+  // Starts the loads of tile j (in order); returns its key mask.
+  auto issue = [&](int j, int st) -> uint32_t {
+    if (j >= n_run) return 0;
+    if ((j & 31) == 0 && j > 0) {
+      page_now = page_next;
+      rows_now = rows_next;
     }
-    if (lane == 0) sm.mask[warp][st] = mask;
-    if (mask == 0) return;  // nothing to load and nothing read
-    const int row_in = key0 & ((1 << p.ps_shift) - 1);
+    if ((j & 31) == 16) locate((j & ~31) + 32, page_next, rows_next);  // arrives in time
+    const int page = __shfl_sync(0xffffffffu, page_now, j & 31);
+    const uint32_t rows = __shfl_sync(0xffffffffu, rows_now, j & 31);
+    const uint32_t mask = page >= 0 && page < p.n_pages ? rows & 0xFFFFu : 0u;
+    if (mask == 0) return 0;  // nothing to load and nothing read
+    const int row_in = rows >> 16;
     const uint8_t* kb = khead + (int64_t)page * p.kp.page + row_in * p.kp.row;
     const uint8_t* vb = vhead + (int64_t)page * p.vp.page + row_in * p.vp.row;
     const uint32_t ks = smem_u32(kst + st * kStageBytes), vs = smem_u32(vst + st * kStageBytes);
@@ -239,16 +249,15 @@ __device__ __forceinline__ void attend_run(const PagedAttnParams& p, AttnSmem<E4
       kb += kRows * p.kp.row;
       vb += kRows * p.vp.row;
     }
+    return mask;
   };
 
-  int key0, page;
-#pragma unroll 1
+  uint32_t masks[kStages - 1];  // of the tiles in flight
+#pragma unroll
   for (int s = 0; s < kStages - 1; ++s) {
-    locate(s, key0, page);
-    if (s < n_run) issue(s, key0, page);
+    masks[s] = issue(s, s);
     cp_async_commit();
   }
-  locate(kStages - 1, key0, page);
 
   // ---- query heads nt * 8 + g as product operands (columns; keys are the rows)
   uint32_t qb[NT][8][2];
@@ -311,10 +320,11 @@ __device__ __forceinline__ void attend_run(const PagedAttnParams& p, AttnSmem<E4
   for (int tt = 0; tt < n_run; ++tt) {
     cp_async_wait<kStages - 2>();
     __syncwarp();
-    if (tt + kStages - 1 < n_run) issue(st_in, key0, page);
+    const uint32_t mask = masks[0];
+#pragma unroll
+    for (int m = 0; m + 2 < kStages; ++m) masks[m] = masks[m + 1];
+    masks[kStages - 2] = issue(tt + kStages - 1, st_in);
     cp_async_commit();
-    locate(tt + kStages, key0, page);  // its table entry arrives during this tile
-    const uint32_t mask = sm.mask[warp][st];
     const uint8_t* kt = kst + st * kStageBytes;
     const uint8_t* vt = vst + st * kStageBytes;
     st = st == kStages - 1 ? 0 : st + 1;
@@ -589,42 +599,47 @@ __global__ void __launch_bounds__(kAttnThreads, WarpStages<E4M3>::kCtasPerSm)
   }
 }
 
-// The same for few and short rows, without a second kernel: a cluster of eight
-// CTAs takes a row, each an equal run of its tiles, and joins them through
-// distributed shared memory in rank order.
-constexpr int kCluster = 8;
+// The same for short rows, without a second kernel: a cluster of up to eight CTAs
+// takes a row, each an equal run of its tiles, and joins them through distributed
+// shared memory in rank order.
+constexpr int kMaxCluster = 8;
 
 template <bool E4M3, bool SEL, int NT>
-__global__ void __cluster_dims__(kCluster, 1, 1)
-    __launch_bounds__(kAttnThreads, WarpStages<E4M3>::kCtasPerSm)
-        paged_attn_short_kernel(const PagedAttnParams p) {
+__global__ void __launch_bounds__(kAttnThreads, WarpStages<E4M3>::kCtasPerSm)
+    paged_attn_short_kernel(const PagedAttnParams p, const int csize) {
   griddep_wait();
   namespace cg = cooperative_groups;
   extern __shared__ __align__(128) unsigned char smem_raw[];
   AttnSmem<E4M3>& sm = *reinterpret_cast<AttnSmem<E4M3>*>(smem_raw);
   __shared__ __align__(16) float part[16][kPartRow];  // m, l, pad, o of this CTA's run
   const cg::cluster_group cluster = cg::this_cluster();
-  const int row = blockIdx.x / kCluster, rank = blockIdx.x % kCluster;
+  const int row = blockIdx.x / csize, rank = blockIdx.x % csize;
   const int b = row / p.Hkv, i = row % p.Hkv, tid = threadIdx.x;
   const int len = paged_len(p, b), groups = row_groups<SEL>(p, b, i, len);
   const int tiles = tiles_of(groups);
-  const int t0 = (int)((int64_t)tiles * rank / kCluster);
+  const int t0 = (int)((int64_t)tiles * rank / csize);
   attend_run<E4M3, SEL, NT>(p, sm, b, i, len, groups, t0,
-                            (int)((int64_t)tiles * (rank + 1) / kCluster) - t0);
+                            (int)((int64_t)tiles * (rank + 1) / csize) - t0);
   for (int r = 0; r < p.G; ++r) {
     float M, l, o;
     join_warps<E4M3>(sm, r, tid, M, l, o);
+    if (csize == 1) {
+      store_final(p, b, p.head[i], r, tid, M, l, o);
+      continue;
+    }
     part[r][4 + tid] = o;
     if (tid == 0) {
       part[r][0] = M;
       part[r][1] = l;
     }
   }
+  if (csize == 1) return;
   cluster.sync();
-  for (int r = rank; r < p.G; r += kCluster) {
-    float m[kCluster], l[kCluster], o[kCluster], M = -INFINITY;
+  for (int r = rank; r < p.G; r += csize) {
+    float m[kMaxCluster], l[kMaxCluster], o[kMaxCluster], M = -INFINITY;
 #pragma unroll
-    for (int c = 0; c < kCluster; ++c) {
+    for (int c = 0; c < kMaxCluster; ++c) {
+      if (c >= csize) continue;
       const float* x = cluster.map_shared_rank(&part[r][0], c);
       m[c] = x[0];
       l[c] = x[1];
@@ -634,7 +649,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1)
     const float m0 = M == -INFINITY ? 0.f : M;
     float ls = 0.f, os = 0.f;
 #pragma unroll
-    for (int c = 0; c < kCluster; ++c) {
+    for (int c = 0; c < kMaxCluster; ++c) {
+      if (c >= csize) continue;
       const float f = m[c] == -INFINITY && l[c] == l[c] ? 0.f : ex2(m[c] - m0);
       ls += f * l[c];
       os += f * o[c];
@@ -700,25 +716,43 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const PagedAttnParams p
 constexpr int kSms = 148;
 constexpr int kMaxAttnCtas = 3 * kSms;
 
-// Clusters of eight suit rows of up to 128 tiles (in a request as long as its
-// table allows), while all clusters are on the GPU at once.
-constexpr int kShortTiles = 128;
+// CTAs of a row's cluster (as many as fit on the GPU at once), 0 for the split over
+// all CTAs.  max_tiles: the longest row's, as far as the host can tell.  Up to 16
+// tiles (1024 keys) a CTA a cluster saves the second kernel and the search for the
+// run's row: 32 rows of 2000 keys 10.1 us against 12.0 (bf16), 256 rows of 500 keys
+// 15.7 against 21.5, of ragged lengths up to 1000 17.5 against 31.5.  Beyond, one long
+// request among short ones would leave most CTAs idle: with 8 of 32 rows longer than
+// the others (131072 keys against 4100) 133 us against 94.
+inline int short_cluster(int64_t rows, int max_tiles, int ctas) {
+  int c = kMaxCluster;
+  while (c > 1 && rows * c > ctas) c >>= 1;
+  return rows * c <= ctas && max_tiles <= 16 * c ? c : 0;
+}
 
 template <bool E4M3, bool SEL, int NT>
 rtp_status launch(const PagedAttnParams& p, int max_tiles, cudaStream_t s) {
   const size_t smem = sizeof(AttnSmem<E4M3>);
   constexpr int ctas = WarpStages<E4M3>::kCtasPerSm * kSms;
   static_assert(ctas <= kMaxAttnCtas, "the workspace holds every CTA's partials");
-  const bool brief = max_tiles <= kShortTiles && (int64_t)p.B * p.Hkv * kCluster <= ctas;
-  auto* kernel = brief ? paged_attn_short_kernel<E4M3, SEL, NT> : paged_attn_kernel<E4M3, SEL, NT>;
+  const int c = short_cluster((int64_t)p.B * p.Hkv, max_tiles, ctas);
+  rtp_status st;
+  if (c > 0) {
+    auto* kernel = paged_attn_short_kernel<E4M3, SEL, NT>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
+        cudaSuccess)
+      return RTP_ERR_CUDA;
+    TraceScope tr("paged_attn", s);
+    return check_cuda(launch_dependent_cluster(kernel, dim3(p.B * p.Hkv * c), dim3(kAttnThreads), c,
+                                               smem, s, p, c));
+  }
+  auto* kernel = paged_attn_kernel<E4M3, SEL, NT>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
       cudaSuccess)
     return RTP_ERR_CUDA;
-  rtp_status st;
   {
     TraceScope tr("paged_attn", s);
-    if ((st = check_cuda(launch_dependent(kernel, dim3(brief ? p.B * p.Hkv * kCluster : ctas),
-                                          dim3(kAttnThreads), smem, s, p))) != RTP_OK || brief)
+    if ((st = check_cuda(launch_dependent(kernel, dim3(ctas), dim3(kAttnThreads), smem, s, p))) !=
+        RTP_OK)
       return st;
   }
   TraceScope tr("paged_join", s);

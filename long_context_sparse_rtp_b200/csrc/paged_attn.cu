@@ -599,12 +599,12 @@ __global__ void __launch_bounds__(kAttnThreads, WarpStages<E4M3>::kCtasPerSm)
   }
 }
 
-// The same for short rows, without a second kernel: a cluster of up to eight CTAs
+// The same for short rows, without a second kernel: a cluster of up to 16 CTAs
 // takes a row, each an equal run of its tiles, and joins them through distributed
 // shared memory in rank order.
-constexpr int kMaxCluster = 8;
-
-template <bool E4M3, bool SEL, int NT>
+//
+// MAXC: 8, or 16 (a larger loop over the CTAs' parts, which costs every size).
+template <bool E4M3, bool SEL, int NT, int MAXC>
 __global__ void __launch_bounds__(kAttnThreads, WarpStages<E4M3>::kCtasPerSm)
     paged_attn_short_kernel(const PagedAttnParams p, const int csize) {
   griddep_wait();
@@ -636,9 +636,9 @@ __global__ void __launch_bounds__(kAttnThreads, WarpStages<E4M3>::kCtasPerSm)
   if (csize == 1) return;
   cluster.sync();
   for (int r = rank; r < p.G; r += csize) {
-    float m[kMaxCluster], l[kMaxCluster], o[kMaxCluster], M = -INFINITY;
+    float m[MAXC], l[MAXC], o[MAXC], M = -INFINITY;
 #pragma unroll
-    for (int c = 0; c < kMaxCluster; ++c) {
+    for (int c = 0; c < MAXC; ++c) {
       if (c >= csize) continue;
       const float* x = cluster.map_shared_rank(&part[r][0], c);
       m[c] = x[0];
@@ -649,7 +649,7 @@ __global__ void __launch_bounds__(kAttnThreads, WarpStages<E4M3>::kCtasPerSm)
     const float m0 = M == -INFINITY ? 0.f : M;
     float ls = 0.f, os = 0.f;
 #pragma unroll
-    for (int c = 0; c < kMaxCluster; ++c) {
+    for (int c = 0; c < MAXC; ++c) {
       if (c >= csize) continue;
       const float f = m[c] == -INFINITY && l[c] == l[c] ? 0.f : ex2(m[c] - m0);
       ls += f * l[c];
@@ -723,8 +723,12 @@ constexpr int kMaxAttnCtas = 3 * kSms;
 // 15.7 against 21.5, of ragged lengths up to 1000 17.5 against 31.5.  Beyond, one long
 // request among short ones would leave most CTAs idle: with 8 of 32 rows longer than
 // the others (131072 keys against 4100) 133 us against 94.
+// Sixteen, with an SM for each CTA, suit the longer of few rows (4 rows: 4000 keys 9.6 us
+// with eight, 8.0 with sixteen; 16000 keys 13.3 against 16.0 over all CTAs), but start
+// more slowly (517 keys: 5.5 and 6.4 us).
 inline int short_cluster(int64_t rows, int max_tiles, int ctas) {
-  int c = kMaxCluster;
+  if (rows * 16 <= kSms && max_tiles > 64) return max_tiles <= 256 ? 16 : 0;
+  int c = 8;
   while (c > 1 && rows * c > ctas) c >>= 1;
   return rows * c <= ctas && max_tiles <= 16 * c ? c : 0;
 }
@@ -737,9 +741,12 @@ rtp_status launch(const PagedAttnParams& p, int max_tiles, cudaStream_t s) {
   const int c = short_cluster((int64_t)p.B * p.Hkv, max_tiles, ctas);
   rtp_status st;
   if (c > 0) {
-    auto* kernel = paged_attn_short_kernel<E4M3, SEL, NT>;
+    auto* kernel = c > 8 ? paged_attn_short_kernel<E4M3, SEL, NT, 16>
+                         : paged_attn_short_kernel<E4M3, SEL, NT, 8>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-        cudaSuccess)
+            cudaSuccess ||
+        (c > 8 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
+                      cudaSuccess))
       return RTP_ERR_CUDA;
     TraceScope tr("paged_attn", s);
     return check_cuda(launch_dependent_cluster(kernel, dim3(p.B * p.Hkv * c), dim3(kAttnThreads), c,

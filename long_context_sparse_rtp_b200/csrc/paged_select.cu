@@ -35,10 +35,10 @@ struct SelectParams {
   const float* bound_scale;   // [n_pages][n_rkv]
   const int32_t* table; int64_t table_stride;
   const int32_t* seq_lens;
-  uint32_t* keys;             // [B][n_rkv][width]: ordered score keys
+  uint32_t* keys;             // [B][n_rkv][pitch]: ordered score keys
   int32_t* sel;               // [B][n_rkv][n_sel]
   int32_t* count;             // [B][n_rkv]
-  int32_t n_pages, width, ps_shift, G, n_rkv, n_sel, n_first, n_recent;
+  int32_t n_pages, width, pitch, ps_shift, G, n_rkv, n_sel, n_first, n_recent;
   int16_t head[kMaxHeads];
 };
 
@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kScoreThreads) paged_score_kernel(const Select
       const int pe = p0 + warp * 16 + s * 8 + g;
       if (t == 0 && pe < p_end) {
         if (pe < p.n_first || pe >= nb - p.n_recent) x = INFINITY;
-        p.keys[(int64_t)row * p.width + pe] = score_key(x + 0.f);  // -0 and 0 are one score
+        p.keys[(int64_t)row * p.pitch + pe] = score_key(x + 0.f);  // -0 and 0 are one score
       }
     }
     if (!more) return;
@@ -217,88 +217,114 @@ __device__ __forceinline__ int block_count(int v, int (*sums)[32], int& turn) {
   return all;
 }
 
+// Inclusive scan over the block.
+__device__ __forceinline__ int block_scan(int v, int* sums) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += y;
+  }
+  if (lane == 31) sums[warp] = v;
+  __syncthreads();
+  return v + __reduce_add_sync(0xffffffffu, lane < warp ? sums[lane] : 0);
+}
+
 constexpr int kTopBins = 2048;
 constexpr int kTopCand = 1024;
 
-// One CTA per row.  E > 0: thread i of warp w holds keys w * 32 E + 32 e + lane;
-// E == 0 (longer rows): the keys are read again from L2 on every pass.
+// One CTA per row; a thread has E consecutive keys in registers, or, E == 0 (longer
+// rows), reads its share again from L2 on every pass.
 //
 // The n-th largest key: 2046 equal bins over the row's finite scores, one for
 // those at +inf and one for -inf; the bin that holds it is found by a scan of the
 // counts, and its few keys are ranked against one another.  The bin is a
 // non-decreasing function of the score however its arithmetic rounds, so the
 // result is exact.  A bin of more than 1024 keys (mass ties) is settled bit by
-// bit instead.  Bound by latency: 32 rounds bit by bit took 14 us for 2048 pages and 24
-// for 16384 (traced, with 6 us of events).
+// bit instead.  Bound by latency: a kernel of 2048 pages takes 2.5 us beyond a
+// launch.
 template <int WARPS, int E>
 __global__ void __launch_bounds__(WARPS * 32) paged_topn_kernel(const SelectParams p) {
-  griddep_wait();
   constexpr int kThreads = WARPS * 32;
-  __shared__ int sums[2][32];
-  __shared__ int base_gt[32], base_eq[32];
+  __shared__ int sums[2][32], scan1[32], scan2[32];
   __shared__ float wlo[32], whi[32];
   __shared__ int hist[kTopBins];
   __shared__ __align__(16) uint32_t cand[kTopCand];
   __shared__ int n_cand, bin_at, bin_above;
   __shared__ uint32_t cut;
-  const int row = blockIdx.x, b = row / p.n_rkv;
-  const int nb = blocks_of(p, b), n = p.n_sel;
+  const int row = blockIdx.x, b = row / p.n_rkv, n = p.n_sel;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int i = tid; i < kTopBins; i += kThreads) hist[i] = 0;
+  if (tid == 0) n_cand = 0;
+  griddep_wait();
+  const int nb = blocks_of(p, b);
   int32_t* sel = p.sel + (int64_t)row * n;
   if (tid == 0) p.count[row] = min(nb, n);
   if (nb <= n) {
     for (int i = tid; i < n; i += kThreads) sel[i] = i < nb ? i : -1;
     return;
   }
-  const uint32_t* keys = p.keys + (int64_t)row * p.width;
-  const int steps = E > 0 ? E : (nb + kThreads - 1) / kThreads;
-  const int w0 = warp * 32 * steps + lane;  // this thread's first key
-  // a real key is never 0 (-inf maps above it)
-  uint32_t kreg[E > 0 ? E : 1];
-  if (E > 0) {
-#pragma unroll
-    for (int e = 0; e < E; ++e) kreg[e] = w0 + 32 * e < nb ? keys[w0 + 32 * e] : 0u;
-  }
-  auto key_at = [&](int e) -> uint32_t {
-    if (E > 0) return kreg[E > 0 ? e : 0];
-    return w0 + 32 * e < nb ? keys[w0 + 32 * e] : 0u;
+  const uint32_t* keys = p.keys + (int64_t)row * p.pitch;
+  const int per = E > 0 ? E : ((nb + kThreads - 1) / kThreads + 3) & ~3;  // keys of a thread
+  const int k0 = tid * per;
+  auto load4 = [&](int e, uint32_t (&k)[4]) {  // keys k0 + e ..; 0 behind the last (-inf is above)
+    uint4 w = make_uint4(0u, 0u, 0u, 0u);
+    if (k0 + e < nb) w = *reinterpret_cast<const uint4*>(keys + k0 + e);
+    k[0] = w.x;
+    k[1] = k0 + e + 1 < nb ? w.y : 0u;
+    k[2] = k0 + e + 2 < nb ? w.z : 0u;
+    k[3] = k0 + e + 3 < nb ? w.w : 0u;
   };
-  for (int i = tid; i < kTopBins; i += kThreads) hist[i] = 0;
-  if (tid == 0) n_cand = 0;
+  uint32_t kreg[E > 0 ? E / 4 : 1][4];
+  if constexpr (E > 0) {
+#pragma unroll
+    for (int e = 0; e < E / 4; ++e) load4(4 * e, kreg[e]);
+  }
+  auto each = [&](auto f) {  // f(e, key e of this thread)
+    if constexpr (E > 0) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) f(e, kreg[e / 4][e & 3]);
+    } else {
+      for (int e = 0; e < per; e += 4) {
+        uint32_t k[4];
+        load4(e, k);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f(e + i, k[i]);
+      }
+    }
+  };
 
   // range of the finite scores
   const uint32_t key_pinf = score_key(INFINITY), key_ninf = score_key(-INFINITY);
-  float lo = INFINITY, hi = -INFINITY;
-#pragma unroll
-  for (int e = 0; e < steps; ++e) {
-    const uint32_t k = key_at(e);
-    if (k > key_ninf && k < key_pinf) {
-      const float x = key_score(k);
-      lo = fminf(lo, x);
-      hi = fmaxf(hi, x);
-    }
-  }
-  lo = -warp_max(-lo);
-  hi = warp_max(hi);
+  uint32_t kmin = 0xFFFFFFFFu, kmax = 0u;
+  each([&](int, uint32_t k) {
+    const bool finite = k > key_ninf && k < key_pinf;
+    kmin = min(kmin, finite ? k : 0xFFFFFFFFu);
+    kmax = max(kmax, finite ? k : 0u);
+  });
+  kmin = __reduce_min_sync(0xffffffffu, kmin);
+  kmax = __reduce_max_sync(0xffffffffu, kmax);
   if (lane == 0) {
-    wlo[warp] = lo;
-    whi[warp] = hi;
+    wlo[warp] = __uint_as_float(kmin);
+    whi[warp] = __uint_as_float(kmax);
   }
   __syncthreads();
-  lo = -warp_max(lane < WARPS ? -wlo[lane] : -INFINITY);
-  hi = warp_max(lane < WARPS ? whi[lane] : -INFINITY);
-  const float half_lo = 0.5f * lo, range = 0.5f * hi - half_lo;  // halves: no overflow
-  const float per = range > 0.f ? fminf((kTopBins - 3) / range, 3.402823466e38f) : 0.f;
+  kmin = __reduce_min_sync(0xffffffffu, lane < WARPS ? __float_as_uint(wlo[lane]) : 0xFFFFFFFFu);
+  kmax = __reduce_max_sync(0xffffffffu, lane < WARPS ? __float_as_uint(whi[lane]) : 0u);
+  const bool some = kmin <= kmax;
+  const float half_lo = some ? 0.5f * key_score(kmin) : 0.f;  // halves: no overflow
+  const float range = some ? 0.5f * key_score(kmax) - half_lo : 0.f;
+  const float scale = range > 0.f ? fminf((kTopBins - 3) / range, 3.402823466e38f) : 0.f;
   auto bin_of = [&](uint32_t k) -> int {
-    if (k >= key_pinf) return kTopBins - 1;
-    if (k <= key_ninf) return 0;
-    return 1 + (int)fminf((0.5f * key_score(k) - half_lo) * per, (float)(kTopBins - 3));
+    const int mid = 1 + (int)fminf((0.5f * key_score(k) - half_lo) * scale, (float)(kTopBins - 3));
+    return k >= key_pinf ? kTopBins - 1 : k <= key_ninf ? 0 : mid;
   };
-#pragma unroll
-  for (int e = 0; e < steps; ++e) {
-    const uint32_t k = key_at(e);
-    if (k) atomicAdd(&hist[bin_of(k)], 1);
-  }
+  uint32_t bins[E > 0 ? E / 2 : 1] = {};  // two to a register
+  each([&](int e, uint32_t k) {
+    const int at = bin_of(k);
+    if constexpr (E > 0) bins[e / 2] = e & 1 ? bins[e / 2] | (uint32_t)at << 16 : (uint32_t)at;
+    if (k) atomicAdd(&hist[at], 1);
+  });
   __syncthreads();
 
   // the bin that holds the n-th largest: a thread has kTopBins / kThreads bins
@@ -306,16 +332,7 @@ __global__ void __launch_bounds__(WARPS * 32) paged_topn_kernel(const SelectPara
   int own = 0;
 #pragma unroll
   for (int i = 0; i < kOwn; ++i) own += hist[tid * kOwn + i];
-  int upto = own;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, upto, o);
-    if (lane >= o) upto += y;
-  }
-  if (lane == 31) base_gt[warp] = upto;
-  __syncthreads();
-  upto += __reduce_add_sync(0xffffffffu, lane < warp ? base_gt[lane] : 0);
-  int above = nb - upto;  // keys in the bins of higher threads
+  int above = nb - block_scan(own, scan1);  // keys in the bins of higher threads
   if (above < n && n <= above + own) {
 #pragma unroll
     for (int i = kOwn - 1; i >= 0; --i) {
@@ -331,11 +348,14 @@ __global__ void __launch_bounds__(WARPS * 32) paged_topn_kernel(const SelectPara
   const int bin = bin_at, among = n - bin_above, in_bin = hist[bin];
   uint32_t T = 0;
   if (in_bin <= kTopCand) {
-#pragma unroll
-    for (int e = 0; e < steps; ++e) {
-      const uint32_t k = key_at(e);
-      if (k && bin_of(k) == bin) cand[atomicAdd(&n_cand, 1)] = k;
-    }
+    each([&](int e, uint32_t k) {
+      int at;
+      if constexpr (E > 0)
+        at = (bins[e / 2] >> (16 * (e & 1))) & 0xFFFF;
+      else
+        at = bin_of(k);
+      if (k && at == bin) cand[atomicAdd(&n_cand, 1)] = k;
+    });
     __syncthreads();
     for (int i = tid; i < in_bin; i += kThreads) {
       const uint32_t k = cand[i];
@@ -353,52 +373,37 @@ __global__ void __launch_bounds__(WARPS * 32) paged_topn_kernel(const SelectPara
     for (int bit = 31; bit >= 0; --bit) {
       const uint32_t c = T | (1u << bit);
       int cnt = 0;
-#pragma unroll
-      for (int e = 0; e < steps; ++e) cnt += key_at(e) >= c;
+      each([&](int, uint32_t k) { cnt += k >= c; });
       if (block_count<WARPS>(cnt, sums, turn) >= n) T = c;
     }
-    __syncthreads();
   }
   // keys above T all stay; of those equal to T the first ones
   int gt = 0, eq = 0;
-#pragma unroll
-  for (int e = 0; e < steps; ++e) {
-    const uint32_t k = key_at(e);
+  each([&](int, uint32_t k) {
     gt += k > T;
     eq += k == T;
-  }
-  const int wg = __reduce_add_sync(0xffffffffu, gt), we = __reduce_add_sync(0xffffffffu, eq);
-  if (lane == 0) {
-    base_gt[warp] = wg;
-    base_eq[warp] = we;
-  }
+  });
+  int gt_at = block_scan(gt, scan2) - gt;
   __syncthreads();
-  int bg = 0, be = 0, all_gt = 0;
-  for (int w = 0; w < WARPS; ++w) {
-    if (w < warp) {
-      bg += base_gt[w];
-      be += base_eq[w];
-    }
-    all_gt += base_gt[w];
-  }
+  int eq_at = block_scan(eq, scan1) - eq;
+  __shared__ int all_gt;
+  if (tid == kThreads - 1) all_gt = gt_at + gt;
+  __syncthreads();
   const int need = n - all_gt;
-  const uint32_t below = (1u << lane) - 1u;
-#pragma unroll
-  for (int e = 0; e < steps; ++e) {
-    const uint32_t k = key_at(e);
-    const uint32_t mg = __ballot_sync(0xffffffffu, k > T), me = __ballot_sync(0xffffffffu, k == T);
-    const int eq_before = be + __popc(me & below);
-    const bool keep = k > T || (k == T && eq_before < need);
-    if (keep) sel[bg + __popc(mg & below) + min(eq_before, need)] = w0 + 32 * e;
-    bg += __popc(mg);
-    be += __popc(me);
-  }
+  each([&](int e, uint32_t k) {
+    const bool above_cut = k > T, at_cut = k == T;
+    if (above_cut || (at_cut && eq_at < need)) sel[gt_at + min(eq_at, need)] = k0 + e;
+    gt_at += above_cut;
+    eq_at += at_cut;
+  });
 }
 
 }  // namespace
 
+inline int32_t select_pitch(int32_t width) { return (width + 3) & ~3; }  // whole uint4s a row
+
 size_t paged_select_ws(int32_t rows, int32_t width) {
-  return align_up(kStatusBytes + (size_t)rows * width * 4, 256);
+  return align_up(kStatusBytes + (size_t)rows * select_pitch(width) * 4, 256);
 }
 
 }  // namespace rtp
@@ -444,6 +449,7 @@ extern "C" rtp_status rtp_paged_block_select(
   p.count = sel_count;
   p.n_pages = n_pages;
   p.width = table_width;
+  p.pitch = select_pitch(table_width);
   p.ps_shift = log2_exact(page_size);
   p.G = ph.G;
   p.n_rkv = ph.n_rkv;
@@ -454,10 +460,10 @@ extern "C" rtp_status rtp_paged_block_select(
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (table_width > n_sel) {
     TraceScope tr("paged_score", s);
-    // one block of pages a CTA while the GPU has room for that (four CTAs an SM),
+    // one block of pages a CTA while the GPU has room for that (eight CTAs an SM),
     // else several, which reuse the CTA's query and overlap their loads
     const int64_t blocks = (table_width + kScorePages - 1) / kScorePages;
-    const int rounds = (int)std::min<int64_t>(8, (blocks * rows + 4 * 148 - 1) / (4 * 148));
+    const int rounds = (int)std::min<int64_t>(8, (blocks * rows + 8 * 148 - 1) / (8 * 148));
     const dim3 grid((unsigned)((blocks + rounds - 1) / rounds), (unsigned)rows);
     if ((st = check_cuda(launch_dependent(ph.G <= 8 ? paged_score_kernel<1> : paged_score_kernel<2>,
                                           grid, dim3(kScoreThreads), 0, s, p, rounds))) != RTP_OK)

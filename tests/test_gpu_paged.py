@@ -171,6 +171,44 @@ def test_attn_many_requests():
     m.check(*m.attn(window=9, n_sink=2), 9, 2)
 
 
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("B", [3, 30, 60, 120])
+@pytest.mark.parametrize("H", [4, 32])
+def test_attn_clusters(kv, B, H):
+    """Row counts that give a row 16, 8, 4, 2 and 1 CTAs; one long request, the others ragged."""
+    lens = [(53 * i) % 400 for i in range(B)]
+    lens[B // 2] = 9001 if B == 3 else 1000
+    m = Made(lens, 16, H, (1, 0), kv, seed=B)
+    m.check(*m.attn(window=300, n_sink=3), 300, 3)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("H", [4, 16])
+def test_attn_long_selection(kv, H):
+    """Selected pages beyond what clusters take, beside short and unused rows."""
+    m = Made([30000, 500, 0, 19500], 64, H, (1,), kv, seed=H)
+    g = torch.Generator().manual_seed(H)
+    sel = torch.full((4, 1, 300), -1, dtype=I32)
+    count = torch.zeros(4, 1, dtype=I32)
+    for b, n in enumerate(m.lens):
+        nb = ref.up(n, 64)
+        k = min(300, nb)
+        sel[b, 0, :k] = torch.randperm(nb, generator=g)[:k].sort().values.to(I32)
+        count[b, 0] = k
+    sel, count = sel.to(DEV), count.to(DEV)
+    m.check(*m.attn(sel=sel, sel_count=count), sel=sel, count=count)
+
+
+def test_attn_selection_that_cannot_be_meant():
+    """Columns outside the table or behind the request, and counts outside the list, name no
+    keys."""
+    m = Made([100, 40], 16, 4, (1,), seed=3)
+    sel = ints([[[0, -1, 3, 99]], [[2 ** 31 - 1, 1, 5, 2]]])
+    count = ints([[9], [-2]])
+    o, lse = m.attn(sel=sel, sel_count=count)
+    m.check(o, lse, sel=ints([[[0, 3]], [[0, 0]]]), count=ints([[2], [0]]))
+
+
 def test_attn_scale_outputs_and_strided_q():
     m = Made([100, 7], 16, 8, (1, 1), seed=6)
     big = torch.zeros(2, 1, 3, 8, D, dtype=torch.bfloat16, device=DEV)

@@ -726,11 +726,18 @@ constexpr int kMaxAttnCtas = 3 * kSms;
 // Sixteen, with an SM for each CTA, suit the longer of few rows (4 rows: 4000 keys 9.6 us
 // with eight, 8.0 with sixteen; 16000 keys 13.3 against 16.0 over all CTAs), but start
 // more slowly (517 keys: 5.5 and 6.4 us).
-inline int short_cluster(int64_t rows, int max_tiles, int ctas) {
+// Clusters need their CTAs within one of the GPU's eight groups of SMs: 128 SMs' worth
+// of clusters run at once (36 clusters of 8 at two CTAs an SM take two waves, 12.0
+// against 7.4 us).  8-bit tiles have half the bytes: there 32 a CTA, where the clusters
+// fill half the GPU or more (64 ragged rows up to 6000 keys: 18.9 against 29.8 us).
+inline int short_cluster(int64_t rows, int max_tiles, int per_sm, bool e4m3) {
   if (rows * 16 <= kSms && max_tiles > 64) return max_tiles <= 256 ? 16 : 0;
+  const int slots = per_sm * 128;
   int c = 8;
-  while (c > 1 && rows * c > ctas) c >>= 1;
-  return rows * c <= ctas && max_tiles <= 16 * c ? c : 0;
+  while (c > 1 && rows * c > slots) c >>= 1;
+  if (rows * c > per_sm * kSms) return 0;
+  const int most = e4m3 && rows * c * 2 >= slots ? 32 : 16;
+  return max_tiles <= most * c ? c : 0;
 }
 
 template <bool E4M3, bool SEL, int NT>
@@ -738,7 +745,7 @@ rtp_status launch(const PagedAttnParams& p, int max_tiles, cudaStream_t s) {
   const size_t smem = sizeof(AttnSmem<E4M3>);
   constexpr int ctas = WarpStages<E4M3>::kCtasPerSm * kSms;
   static_assert(ctas <= kMaxAttnCtas, "the workspace holds every CTA's partials");
-  const int c = short_cluster((int64_t)p.B * p.Hkv, max_tiles, ctas);
+  const int c = short_cluster((int64_t)p.B * p.Hkv, max_tiles, WarpStages<E4M3>::kCtasPerSm, E4M3);
   rtp_status st;
   if (c > 0) {
     auto* kernel = c > 8 ? paged_attn_short_kernel<E4M3, SEL, NT, 16>

@@ -70,23 +70,20 @@ __device__ __forceinline__ void s8x4_to_f16(uint32_t x, uint32_t& lo, uint32_t& 
   hi = *reinterpret_cast<const uint32_t*>(&h);
 }
 
-constexpr int kScoreThreads = 256;
-constexpr int kScorePages = 16 * kScoreThreads / 32;  // pages of a CTA at once, 16 a warp
 constexpr int kQRow = kD + 4;  // fp16 elements: eight bytes of padding keep reads on all banks
 
-// CTA (x, row): `rounds` blocks of kScorePages pages of a row.  NT: tiles of 8 heads.
 template <int NT>
-__global__ void __launch_bounds__(kScoreThreads) paged_score_kernel(const SelectParams p,
-                                                                    const int rounds) {
-  griddep_wait();
-  const int row = blockIdx.y, b = row / p.n_rkv, rk = row % p.n_rkv;
-  const int nb = blocks_of(p, b);
-  int p0 = blockIdx.x * rounds * kScorePages;
-  const int p_end = min(nb, p0 + rounds * kScorePages);
-  if (p0 >= p_end || nb <= p.n_sel) return;  // a row that keeps every page needs no scores
-  __shared__ __align__(16) uint16_t q8[2][NT * 8][kQRow];  // min(q8, 0) and max(q8, 0) as fp16
-  __shared__ float sq[NT * 8];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+struct ScoreSmem {
+  __align__(16) uint16_t q8[2][NT * 8][kQRow];  // min(q8, 0) and max(q8, 0) as fp16
+  float sq[NT * 8];
+};
+
+// Scores pages [p0, p_end) of row (b, rk), nb pages long, by a CTA of WARPS warps, 16
+// pages a warp at once: out(page, key) for each.  NT: tiles of 8 heads.
+template <int NT, int WARPS, typename Out>
+__device__ __forceinline__ void score_pages(const SelectParams& p, ScoreSmem<NT>& sm, int b, int rk,
+                                            int nb, int p0, int p_end, Out out) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int32_t* tab = p.table + (int64_t)b * p.table_stride;
 
   // this lane's pages: g and g + 8 of the warp's 16
@@ -115,7 +112,7 @@ __global__ void __launch_bounds__(kScoreThreads) paged_score_kernel(const Select
   locate(p0);
 
   // the G query heads in 8-bit steps, split by sign, a warp a head
-  for (int h = warp; h < NT * 8; h += kScoreThreads / 32) {
+  for (int h = warp; h < NT * 8; h += WARPS) {
     float x[4] = {0.f, 0.f, 0.f, 0.f}, s = 0.f;
     if (h < p.G) {
       const uint2 x2 = *reinterpret_cast<const uint2*>(
@@ -142,21 +139,23 @@ __global__ void __launch_bounds__(kScoreThreads) paged_score_kernel(const Select
     }
 #pragma unroll
     for (int i = 0; i < 4; i += 2) {
-      *reinterpret_cast<uint32_t*>(&q8[0][h][lane * 4 + i]) = neg[i] | ((uint32_t)neg[i + 1] << 16);
-      *reinterpret_cast<uint32_t*>(&q8[1][h][lane * 4 + i]) = pos[i] | ((uint32_t)pos[i + 1] << 16);
+      *reinterpret_cast<uint32_t*>(&sm.q8[0][h][lane * 4 + i]) = neg[i] | ((uint32_t)neg[i + 1] << 16);
+      *reinterpret_cast<uint32_t*>(&sm.q8[1][h][lane * 4 + i]) = pos[i] | ((uint32_t)pos[i + 1] << 16);
     }
-    if (lane == 0) sq[h] = s;
+    if (lane == 0) sm.sq[h] = s;
   }
+  if (warp >= NT * 8) load();
   __syncthreads();
   float sqv[NT][2];  // heads 8 nt + 2 t + {0, 1}
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    sqv[nt][0] = sq[nt * 8 + 2 * t];
-    sqv[nt][1] = sq[nt * 8 + 2 * t + 1];
+    sqv[nt][0] = sm.sq[nt * 8 + 2 * t];
+    sqv[nt][1] = sm.sq[nt * 8 + 2 * t + 1];
   }
 
   for (;;) {
-    locate(p0 + kScorePages);  // the next round's table entries arrive during this one
+    const int next = p0 + 16 * WARPS;
+    locate(next);  // the next round's table entries arrive during this one
     // 16 products of 16 dimensions: word u of the lane's chunk j is its four
     // elements of product 4 j + u, the same dimensions of the query
     float acc[NT][4] = {};
@@ -172,14 +171,13 @@ __global__ void __launch_bounds__(kScoreThreads) paged_score_kernel(const Select
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           const uint2 q = *reinterpret_cast<const uint2*>(
-              &q8[j >> 1][nt * 8 + g][(j & 1) * 64 + t * 16 + u * 4]);
+              &sm.q8[j >> 1][nt * 8 + g][(j & 1) * 64 + t * 16 + u * 4]);
           mma_f16(acc[nt], a0, a1, a2, a3, q.x, q.y);
         }
       }
     }
     const float spv[2] = {sp[0], sp[1]};
-    const bool more = p0 + kScorePages < p_end;
-    if (more) load();
+    if (next < p_end) load();
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       float x = -INFINITY;
@@ -197,12 +195,31 @@ __global__ void __launch_bounds__(kScoreThreads) paged_score_kernel(const Select
       const int pe = p0 + warp * 16 + s * 8 + g;
       if (t == 0 && pe < p_end) {
         if (pe < p.n_first || pe >= nb - p.n_recent) x = INFINITY;
-        p.keys[(int64_t)row * p.pitch + pe] = score_key(x + 0.f);  // -0 and 0 are one score
+        out(pe, score_key(x + 0.f));  // -0 and 0 are one score
       }
     }
-    if (!more) return;
-    p0 += kScorePages;
+    if (next >= p_end) return;
+    p0 = next;
   }
+}
+
+constexpr int kScoreThreads = 256;
+constexpr int kScorePages = 16 * kScoreThreads / 32;  // pages of a CTA at once
+
+// CTA (x, row): `rounds` blocks of kScorePages pages of a row.
+template <int NT>
+__global__ void __launch_bounds__(kScoreThreads) paged_score_kernel(const SelectParams p,
+                                                                    const int rounds) {
+  griddep_wait();
+  __shared__ ScoreSmem<NT> sm;
+  const int row = blockIdx.y, b = row / p.n_rkv, rk = row % p.n_rkv;
+  const int nb = blocks_of(p, b);
+  const int p0 = blockIdx.x * rounds * kScorePages;
+  const int p_end = min(nb, p0 + rounds * kScorePages);
+  if (p0 >= p_end || nb <= p.n_sel) return;  // a row that keeps every page needs no scores
+  uint32_t* keys = p.keys + (int64_t)row * p.pitch;
+  score_pages<NT, kScoreThreads / 32>(p, sm, b, rk, nb, p0, p_end,
+                                      [&](int i, uint32_t k) { keys[i] = k; });
 }
 
 // Sum over the block of a per-thread count; `sums` holds two buffers in turn.
@@ -230,6 +247,8 @@ __device__ __forceinline__ int block_scan(int v, int* sums) {
   return v + __reduce_add_sync(0xffffffffu, lane < warp ? sums[lane] : 0);
 }
 
+constexpr int kOneWarps = 16;  // of a CTA that scores and selects
+constexpr int kOneKeys = 4;    // keys of its threads
 constexpr int kTopBins = 2048;
 constexpr int kTopCand = 1024;
 
@@ -243,9 +262,15 @@ constexpr int kTopCand = 1024;
 // result is exact.  A bin of more than 1024 keys (mass ties) is settled bit by
 // bit instead.  Bound by latency: a kernel of 2048 pages takes 2.5 us beyond a
 // launch.
-template <int WARPS, int E>
+//
+// NT > 0 (short rows): the CTA scores its row itself first, in tiles of 8 heads, with
+// the keys in shared memory: one kernel.
+template <int WARPS, int E, int NT>
 __global__ void __launch_bounds__(WARPS * 32) paged_topn_kernel(const SelectParams p) {
   constexpr int kThreads = WARPS * 32;
+  constexpr int kHeld = NT > 0 ? kThreads * E : 4;
+  __shared__ ScoreSmem<(NT > 0 ? NT : 1)> score;
+  __shared__ __align__(16) uint32_t held[kHeld];
   __shared__ int sums[2][32], scan1[32], scan2[32];
   __shared__ float wlo[32], whi[32];
   __shared__ int hist[kTopBins];
@@ -264,7 +289,12 @@ __global__ void __launch_bounds__(WARPS * 32) paged_topn_kernel(const SelectPara
     for (int i = tid; i < n; i += kThreads) sel[i] = i < nb ? i : -1;
     return;
   }
-  const uint32_t* keys = p.keys + (int64_t)row * p.pitch;
+  const uint32_t* keys = NT > 0 ? held : p.keys + (int64_t)row * p.pitch;
+  if constexpr (NT > 0) {
+    score_pages<NT, WARPS>(p, score, b, row % p.n_rkv, nb, 0, nb,
+                           [&](int i, uint32_t k) { held[i] = k; });
+    __syncthreads();
+  }
   const int per = E > 0 ? E : ((nb + kThreads - 1) / kThreads + 3) & ~3;  // keys of a thread
   const int k0 = tid * per;
   auto load4 = [&](int e, uint32_t (&k)[4]) {  // keys k0 + e ..; 0 behind the last (-inf is above)
@@ -458,25 +488,34 @@ extern "C" rtp_status rtp_paged_block_select(
   p.n_recent = n_recent;
   memcpy(p.head, ph.head, sizeof(p.head));
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const dim3 grid((unsigned)rows);
+  // A round of pages (256) for a CTA: one kernel, 5.5 us against 7.1.  A second round
+  // takes the gain back, unless the rows fill the GPU: 96 rows of 1000 pages 10.7 us
+  // against 12.1, 256 rows of 2000 29.6 against 38.5.
+  const int64_t rounds_one = std::max<int64_t>(1, std::min<int64_t>(8, rows / 24));
+  if (table_width <= 16 * kOneWarps * rounds_one) {
+    static_assert(16 * kOneWarps * 8 <= kOneWarps * 32 * kOneKeys, "eight rounds' keys fit");
+    TraceScope tr("paged_topn", s);
+    return check_cuda(launch_dependent(ph.G <= 8 ? paged_topn_kernel<kOneWarps, kOneKeys, 1>
+                                                 : paged_topn_kernel<kOneWarps, kOneKeys, 2>,
+                                       grid, dim3(kOneWarps * 32), 0, s, p));
+  }
   if (table_width > n_sel) {
     TraceScope tr("paged_score", s);
     // one block of pages a CTA while the GPU has room for that (eight CTAs an SM),
     // else several, which reuse the CTA's query and overlap their loads
     const int64_t blocks = (table_width + kScorePages - 1) / kScorePages;
     const int rounds = (int)std::min<int64_t>(8, (blocks * rows + 8 * 148 - 1) / (8 * 148));
-    const dim3 grid((unsigned)((blocks + rounds - 1) / rounds), (unsigned)rows);
+    const dim3 blocks2((unsigned)((blocks + rounds - 1) / rounds), (unsigned)rows);
     if ((st = check_cuda(launch_dependent(ph.G <= 8 ? paged_score_kernel<1> : paged_score_kernel<2>,
-                                          grid, dim3(kScoreThreads), 0, s, p, rounds))) != RTP_OK)
+                                          blocks2, dim3(kScoreThreads), 0, s, p, rounds))) != RTP_OK)
       return st;
   }
   // the smallest CTA whose registers hold the row
   TraceScope tr("paged_topn", s);
-  const dim3 grid((unsigned)rows);
-  if (table_width <= 8 * 32 * 4)
-    return check_cuda(launch_dependent(paged_topn_kernel<8, 4>, grid, dim3(256), 0, s, p));
   if (table_width <= 16 * 32 * 8)
-    return check_cuda(launch_dependent(paged_topn_kernel<16, 8>, grid, dim3(512), 0, s, p));
+    return check_cuda(launch_dependent(paged_topn_kernel<16, 8, 0>, grid, dim3(512), 0, s, p));
   if (table_width <= 32 * 32 * 16)
-    return check_cuda(launch_dependent(paged_topn_kernel<32, 16>, grid, dim3(1024), 0, s, p));
-  return check_cuda(launch_dependent(paged_topn_kernel<32, 0>, grid, dim3(1024), 0, s, p));
+    return check_cuda(launch_dependent(paged_topn_kernel<32, 16, 0>, grid, dim3(1024), 0, s, p));
+  return check_cuda(launch_dependent(paged_topn_kernel<32, 0, 0>, grid, dim3(1024), 0, s, p));
 }

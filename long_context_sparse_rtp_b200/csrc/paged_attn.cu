@@ -726,6 +726,7 @@ constexpr int kMaxAttnCtas = 3 * kSms;
 // Sixteen, with an SM for each CTA, suit the longer of few rows (4 rows: 4000 keys 9.6 us
 // with eight, 8.0 with sixteen; 16000 keys 13.3 against 16.0 over all CTAs), but start
 // more slowly (517 keys: 5.5 and 6.4 us).
+// A few tiles are one CTA's (100 keys: 4.0 us, a cluster 5.1).
 // Clusters need their CTAs within one of the GPU's eight groups of SMs: 128 SMs' worth
 // of clusters run at once (36 clusters of 8 at two CTAs an SM take two waves, 12.0
 // against 7.4 us).  8-bit tiles have half the bytes: there 32 a CTA, where the clusters
@@ -733,7 +734,7 @@ constexpr int kMaxAttnCtas = 3 * kSms;
 inline int short_cluster(int64_t rows, int max_tiles, int per_sm, bool e4m3) {
   if (rows * 16 <= kSms && max_tiles > 64) return max_tiles <= 256 ? 16 : 0;
   const int slots = per_sm * 128;
-  int c = 8;
+  int c = max_tiles <= 4 ? 1 : 8;
   while (c > 1 && rows * c > slots) c >>= 1;
   if (rows * c > per_sm * kSms) return 0;
   const int most = e4m3 && rows * c * 2 >= slots ? 32 : 16;

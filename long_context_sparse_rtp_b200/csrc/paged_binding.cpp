@@ -27,6 +27,7 @@ namespace {
 constexpr int64_t kD = 128;
 constexpr int64_t kAny = -1;  // any size
 PyObject* g_error = nullptr;  // RtpError
+PyObject* g_plan_names[6];    // the plan's outputs
 
 struct Bad {  // becomes a ValueError
   std::string what;
@@ -143,11 +144,13 @@ at::Tensor empty(c10::IntArrayRef shape, at::ScalarType type, c10::Device dev) {
   return at::detail::empty_cuda(shape, type, dev, std::nullopt);
 }
 
-// A contiguous tensor on elements from `offset` of buf's storage.
-at::Tensor part(const at::Tensor& buf, int64_t offset, c10::IntArrayRef shape) {
+// A contiguous tensor on buf's storage (32-bit elements) from its element `offset`.
+at::Tensor part(const at::Tensor& buf, int64_t offset, c10::IntArrayRef shape,
+                at::ScalarType type = at::kInt) {
+  const auto meta = c10::scalarTypeToTypeMeta(type);
   at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(buf.storage()),
-                                                          buf.key_set(), buf.dtype());
-  t.unsafeGetTensorImpl()->set_storage_offset(offset);
+                                                          buf.key_set(), meta);
+  t.unsafeGetTensorImpl()->set_storage_offset(offset * 4 / (int64_t)meta.itemsize());
   t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
   return t;
 }
@@ -246,7 +249,7 @@ const int32_t* i32(const at::Tensor& t) { return static_cast<const int32_t*>(ptr
 int32_t* i32_out(const at::Tensor& t) { return static_cast<int32_t*>(ptr(t)); }
 
 // (seq_lens, n_new, block_table, free_pages, free_count, page_size, max_tokens,
-//  row_tokens, release, six buffers or None, stream) -> the six outputs
+//  row_tokens, release, six buffers or None, stream) -> dict of the six outputs
 PyObject* plan(PyObject* const* a) {
   const at::Tensor& lens = cuda_tensor(a[0], "seq_lens");
   const c10::Device dev = lens.device();
@@ -303,9 +306,17 @@ PyObject* plan(PyObject* const* a) {
                        count(out[3].size(0), "spans: too many"), i32_out(out[0]), i32_out(out[1]),
                        i32_out(out[2]), i32_out(out[3]), i32_out(out[4]), i32_out(out[5]),
                        ptr(buf), ws_bytes, raw(on.stream)));
-  PyObject* r = PyTuple_New(6);
+  PyObject* r = PyDict_New();
   if (r == nullptr) throw Set{};
-  for (int i = 0; i < 6; ++i) PyTuple_SET_ITEM(r, i, THPVariable_Wrap(out[i]));
+  for (int i = 0; i < 6; ++i) {
+    PyObject* t = THPVariable_Wrap(out[i]);
+    const bool ok = t != nullptr && PyDict_SetItem(r, g_plan_names[i], t) == 0;
+    Py_XDECREF(t);
+    if (!ok) {
+      Py_DECREF(r);
+      throw Set{};
+    }
+  }
   return r;
 }
 
@@ -369,9 +380,12 @@ PyObject* block_select(PyObject* const* a) {
   const int32_t n_sel = to_int(a[7], "n_sel");
   need(n_sel >= 1, "n_sel: expected at least 1");
   On on(dev, a[12]);
-  const at::Tensor sel = none(a[10]) ? empty({B, role.n_rkv, n_sel}, at::kInt, dev)
+  const int64_t n_rows = (int64_t)B * role.n_rkv;
+  at::Tensor buf;  // the outputs' one allocation
+  if (none(a[10]) || none(a[11])) buf = empty({n_rows * (n_sel + (int64_t)1)}, at::kInt, dev);
+  const at::Tensor sel = none(a[10]) ? part(buf, 0, {B, role.n_rkv, n_sel})
                                      : tensor(a[10], "sel", at::kInt, {B, role.n_rkv, n_sel}, dev);
-  const at::Tensor n = none(a[11]) ? empty({B, role.n_rkv}, at::kInt, dev)
+  const at::Tensor n = none(a[11]) ? part(buf, n_rows * n_sel, {B, role.n_rkv})
                                    : tensor(a[11], "sel_count", at::kInt, {B, role.n_rkv}, dev);
   Workspace ws(RTP_PAGED_SELECT, B, H, &role, tab.width);
   check("rtp_paged_block_select",
@@ -411,10 +425,14 @@ PyObject* attn_decode(PyObject* const* a) {
   }
   const float scale = (float)to_double(a[12]);
   On on(dev, a[15]);
-  const at::Tensor o = none(a[13]) ? empty({B, 1, H, kD}, at::kBFloat16, dev) : cuda_tensor(a[13], "o");
+  const int64_t o_ints = (int64_t)B * H * (kD / 2);
+  at::Tensor buf;  // the outputs' one allocation
+  if (none(a[13]) || none(a[14])) buf = empty({o_ints + (int64_t)B * H}, at::kInt, dev);
+  const at::Tensor o =
+      none(a[13]) ? part(buf, 0, {B, 1, H, kD}, at::kBFloat16) : cuda_tensor(a[13], "o");
   Rows orow = {ptr(o), H * kD};
   if (!none(a[13])) orow = rows(a[13], "o", B, H, dev, true);
-  const at::Tensor lse = none(a[14]) ? empty({B, H, 1}, at::kFloat, dev)
+  const at::Tensor lse = none(a[14]) ? part(buf, o_ints, {B, H, 1}, at::kFloat)
                                      : tensor(a[14], "lse", at::kFloat, {B, H, 1}, dev);
   Workspace ws(RTP_PAGED_ATTN, B, H, &role, tab.width);
   check("rtp_paged_attn_decode",
@@ -469,4 +487,9 @@ PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_paged", nullptr, -1, g_methods}
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__paged(void) { return PyModule_Create(&g_module); }
+PyMODINIT_FUNC PyInit__paged(void) {
+  const char* names[6] = {"seq_lens", "cu_new", "slot_map", "spans", "free_count", "admitted"};
+  for (int i = 0; i < 6; ++i)
+    if ((g_plan_names[i] = PyUnicode_InternFromString(names[i])) == nullptr) return nullptr;
+  return PyModule_Create(&g_module);
+}

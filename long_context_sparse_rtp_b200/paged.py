@@ -57,9 +57,8 @@ def rtp_paged_plan(seq_lens, n_new, block_table, free_pages, free_count, *, page
         bufs = [out.get(name) for name in _PLAN]
     else:
         raise ValueError(f"out: expected some of {list(_PLAN)}")
-    return dict(zip(_PLAN, (_ext or _native()).plan(
-        seq_lens, n_new, block_table, free_pages, free_count, page_size, max_tokens, row_tokens,
-        release, *bufs, stream)))
+    return (_ext or _native()).plan(seq_lens, n_new, block_table, free_pages, free_count, page_size,
+                                    max_tokens, row_tokens, release, *bufs, stream)
 
 
 def rtp_paged_kv_write(k, v, slot_map, k_pages, v_pages, *, k_scale=None, v_scale=None,

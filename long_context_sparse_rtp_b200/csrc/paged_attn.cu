@@ -53,8 +53,8 @@ struct PagedAttnParams {
   int16_t head[kMaxHeads];
 };
 
-constexpr int kAttnThreads = 128;
-constexpr int kAttnWarps = kAttnThreads / 32;
+constexpr int kAttnWarps = 4;  // of a CTA of the split over all CTAs; a tile is a group each
+constexpr int kAttnThreads = kAttnWarps * 32;
 
 // Tokens of request b, as far as its table can hold them.
 __device__ __forceinline__ int paged_len(const PagedAttnParams& p, int b) {
@@ -146,15 +146,23 @@ struct WarpStages {
   uint8_t v[kStages][kGroup][kRow];
 };
 
-template <bool E4M3>
+template <bool E4M3, int WARPS>
 struct AttnSmem {
-  WarpStages<E4M3> w[kAttnWarps];  // a finished run's partial outputs reuse each warp's stages
-  float wm[kAttnWarps][16], wl[kAttnWarps][16];
-  int64_t sums[kAttnWarps], first;
+  WarpStages<E4M3> w[WARPS];  // a finished run's partial outputs reuse each warp's stages
+  float wm[WARPS][16], wl[WARPS][16];
+  int64_t sums[WARPS], first;
   int req;
 };
-static_assert(sizeof(WarpStages<true>) >= 16 * kD * 4, "partials fit a warp's stages");
-static_assert(sizeof(WarpStages<false>) >= 16 * kD * 4, "partials fit a warp's stages");
+// A finished run's outputs in a warp's stages: rows of heads, padded so that the
+// quads' stores fall on different banks.
+template <bool E4M3>
+constexpr int kOutRow = E4M3 ? 148 : 132;
+template <bool E4M3>
+__device__ __forceinline__ int out_at(int r, int d) {
+  return r * kOutRow<E4M3> + d + (E4M3 ? 2 * (d >> 4) : 0);
+}
+static_assert(sizeof(WarpStages<true>) >= 16 * kOutRow<true> * 4, "partials fit a warp's stages");
+static_assert(sizeof(WarpStages<false>) >= 16 * kOutRow<false> * 4, "partials fit a warp's stages");
 
 // Where a run's results go: o and lse, or a partial.
 __device__ __forceinline__ void store_final(const PagedAttnParams& p, int b, int g, int r, int d,
@@ -170,9 +178,9 @@ __device__ __forceinline__ void store_final(const PagedAttnParams& p, int b, int
 // Tiles [t0, t0 + n_run) of row i of request b by this CTA: leaves each warp's
 // maximum, sum and outputs in shared memory, after a barrier.  NT: tiles of 8 query
 // heads (1 for G <= 8).
-template <bool E4M3, bool SEL, int NT>
-__device__ __forceinline__ void attend_run(const PagedAttnParams& p, AttnSmem<E4M3>& sm, int b,
-                                           int i, int len, int groups, int t0, int n_run) {
+template <bool E4M3, bool SEL, int NT, int WARPS>
+__device__ __forceinline__ void attend_run(const PagedAttnParams& p, AttnSmem<E4M3, WARPS>& sm,
+                                           int b, int i, int len, int groups, int t0, int n_run) {
   constexpr int kRow = WarpStages<E4M3>::kRow, kStages = WarpStages<E4M3>::kStages;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
@@ -193,7 +201,7 @@ __device__ __forceinline__ void attend_run(const PagedAttnParams& p, AttnSmem<E4
   // where there is none), and its first row in the page with the keys that count
   // (bit r of the low half: key r of the group).
   auto locate = [&](int first, int& page, uint32_t& rows) {
-    const int tt = first + lane, gi = kAttnWarps * (t0 + tt) + warp;
+    const int tt = first + lane, gi = WARPS * (t0 + tt) + warp;
     page = -1;
     rows = 0;
     if (tt >= n_run || gi >= groups) return;
@@ -472,8 +480,13 @@ __device__ __forceinline__ void attend_run(const PagedAttnParams& p, AttnSmem<E4
         }
 #pragma unroll
         for (int d = 0; d < 8; ++d) {
-          wo[r * kD + (E4M3 ? 16 * g + 2 * d : 16 * d + g)] = oacc[nt][d][c];
-          wo[r * kD + (E4M3 ? 16 * g + 2 * d + 1 : 16 * d + g + 8)] = oacc[nt][d][2 + c];
+          if (E4M3) {
+            *reinterpret_cast<float2*>(wo + out_at<true>(r, 16 * g + 2 * d)) =
+                make_float2(oacc[nt][d][c], oacc[nt][d][2 + c]);
+          } else {
+            wo[out_at<false>(r, 16 * d + g)] = oacc[nt][d][c];
+            wo[out_at<false>(r, 16 * d + g + 8)] = oacc[nt][d][2 + c];
+          }
         }
       }
     }
@@ -481,19 +494,19 @@ __device__ __forceinline__ void attend_run(const PagedAttnParams& p, AttnSmem<E4
 }
 
 // A finished run's result for one query head and dimension: the warps' joined.
-template <bool E4M3>
-__device__ __forceinline__ void join_warps(const AttnSmem<E4M3>& sm, int r, int d, float& M,
+template <bool E4M3, int WARPS>
+__device__ __forceinline__ void join_warps(const AttnSmem<E4M3, WARPS>& sm, int r, int d, float& M,
                                            float& l, float& o) {
   M = -INFINITY;
 #pragma unroll
-  for (int w = 0; w < kAttnWarps; ++w) M = fmaxf(M, sm.wm[w][r]);
+  for (int w = 0; w < WARPS; ++w) M = fmaxf(M, sm.wm[w][r]);
   o = l = 0.f;
 #pragma unroll
-  for (int w = 0; w < kAttnWarps; ++w) {
+  for (int w = 0; w < WARPS; ++w) {
     // a warp that saw no key has l = 0 and o = 0; a NaN score leaves NaN in l and o
     const float f = ex2(sm.wm[w][r] - (M == -INFINITY ? 0.f : M) - kShift<E4M3>);
     const float fw = sm.wm[w][r] == -INFINITY && sm.wl[w][r] == sm.wl[w][r] ? 0.f : f;
-    o += fw * reinterpret_cast<const float*>(&sm.w[w].k[0][0][0])[r * kD + d];
+    o += fw * reinterpret_cast<const float*>(&sm.w[w].k[0][0][0])[out_at<E4M3>(r, d)];
     l += fw * sm.wl[w][r];
   }
 }
@@ -503,7 +516,7 @@ __global__ void __launch_bounds__(kAttnThreads, WarpStages<E4M3>::kCtasPerSm)
     paged_attn_kernel(const PagedAttnParams p) {
   griddep_wait();
   extern __shared__ __align__(128) unsigned char smem_raw[];
-  AttnSmem<E4M3>& sm = *reinterpret_cast<AttnSmem<E4M3>*>(smem_raw);
+  AttnSmem<E4M3, kAttnWarps>& sm = *reinterpret_cast<AttnSmem<E4M3, kAttnWarps>*>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   // ---- this CTA's run of tiles
@@ -577,12 +590,13 @@ __global__ void __launch_bounds__(kAttnThreads, WarpStages<E4M3>::kCtasPerSm)
     const int t1 = (int)min((int64_t)tiles, t0 + (end - pos));
     if (t0 == 0 && tid == 0) p.meta[1 + (int64_t)b * p.Hkv + i] = pos;
 
-    attend_run<E4M3, SEL, NT>(p, sm, b, i, len, groups, t0, t1 - t0);
+    attend_run<E4M3, SEL, NT, kAttnWarps>(p, sm, b, i, len, groups, t0, t1 - t0);
     const bool whole = t0 == 0 && t1 == tiles;
     float* part = p.part + ((int64_t)blockIdx.x * 2 + (pos == start ? 0 : 1)) * p.G * kPartRow;
+#pragma unroll 4
     for (int r = 0; r < p.G; ++r) {
       float M, l, o;
-      join_warps<E4M3>(sm, r, tid, M, l, o);
+      join_warps(sm, r, tid, M, l, o);
       if (whole) {
         store_final(p, b, head, r, tid, M, l, o);
       } else {
@@ -604,25 +618,29 @@ __global__ void __launch_bounds__(kAttnThreads, WarpStages<E4M3>::kCtasPerSm)
 // shared memory in rank order.
 //
 // MAXC: 8, or 16 (a larger loop over the CTAs' parts, which costs every size).
-template <bool E4M3, bool SEL, int NT, int MAXC>
-__global__ void __launch_bounds__(kAttnThreads, WarpStages<E4M3>::kCtasPerSm)
+template <bool E4M3, bool SEL, int NT, int MAXC, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, WARPS > kAttnWarps ? 1 : WarpStages<E4M3>::kCtasPerSm)
     paged_attn_short_kernel(const PagedAttnParams p, const int csize) {
   griddep_wait();
   namespace cg = cooperative_groups;
   extern __shared__ __align__(128) unsigned char smem_raw[];
-  AttnSmem<E4M3>& sm = *reinterpret_cast<AttnSmem<E4M3>*>(smem_raw);
+  AttnSmem<E4M3, WARPS>& sm = *reinterpret_cast<AttnSmem<E4M3, WARPS>*>(smem_raw);
   __shared__ __align__(16) float part[16][kPartRow];  // m, l, pad, o of this CTA's run
   const cg::cluster_group cluster = cg::this_cluster();
   const int row = blockIdx.x / csize, rank = blockIdx.x % csize;
-  const int b = row / p.Hkv, i = row % p.Hkv, tid = threadIdx.x;
+  const int b = row / p.Hkv, i = row % p.Hkv;
+  // a quarter of the warps' threads has the 128 dimensions of one query head
+  constexpr int kParts = WARPS / 4;
+  const int part_of = threadIdx.x >> 7, tid = threadIdx.x & 127;
   const int len = paged_len(p, b), groups = row_groups<SEL>(p, b, i, len);
-  const int tiles = tiles_of(groups);
+  const int tiles = (groups + WARPS - 1) / WARPS;
   const int t0 = (int)((int64_t)tiles * rank / csize);
-  attend_run<E4M3, SEL, NT>(p, sm, b, i, len, groups, t0,
+  attend_run<E4M3, SEL, NT, WARPS>(p, sm, b, i, len, groups, t0,
                             (int)((int64_t)tiles * (rank + 1) / csize) - t0);
-  for (int r = 0; r < p.G; ++r) {
+#pragma unroll 4
+  for (int r = part_of; r < p.G; r += kParts) {
     float M, l, o;
-    join_warps<E4M3>(sm, r, tid, M, l, o);
+    join_warps(sm, r, tid, M, l, o);
     if (csize == 1) {
       store_final(p, b, p.head[i], r, tid, M, l, o);
       continue;
@@ -635,7 +653,7 @@ __global__ void __launch_bounds__(kAttnThreads, WarpStages<E4M3>::kCtasPerSm)
   }
   if (csize == 1) return;
   cluster.sync();
-  for (int r = rank; r < p.G; r += csize) {
+  for (int r = rank + part_of * csize; r < p.G; r += csize * kParts) {
     float m[MAXC], l[MAXC], o[MAXC], M = -INFINITY;
 #pragma unroll
     for (int c = 0; c < MAXC; ++c) {
@@ -741,29 +759,40 @@ inline int short_cluster(int64_t rows, int max_tiles, int per_sm, bool e4m3) {
   return max_tiles <= most * c ? c : 0;
 }
 
+template <bool E4M3, bool SEL, int NT, int MAXC, int WARPS>
+rtp_status launch_short(const PagedAttnParams& p, int c, cudaStream_t s) {
+  const size_t smem = sizeof(AttnSmem<E4M3, WARPS>);
+  auto* kernel = paged_attn_short_kernel<E4M3, SEL, NT, MAXC, WARPS>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
+          cudaSuccess ||
+      (MAXC > 8 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed,
+                                        1) != cudaSuccess))
+    return RTP_ERR_CUDA;
+  TraceScope tr("paged_attn", s);
+  return check_cuda(launch_dependent_cluster(kernel, dim3(p.B * p.Hkv * c), dim3(WARPS * 32), c,
+                                             smem, s, p, c));
+}
+
 template <bool E4M3, bool SEL, int NT>
 rtp_status launch(const PagedAttnParams& p, int max_tiles, cudaStream_t s) {
-  const size_t smem = sizeof(AttnSmem<E4M3>);
-  constexpr int ctas = WarpStages<E4M3>::kCtasPerSm * kSms;
+  const size_t smem = sizeof(AttnSmem<E4M3, kAttnWarps>);
+  constexpr int per_sm = WarpStages<E4M3>::kCtasPerSm, ctas = per_sm * kSms;
   static_assert(ctas <= kMaxAttnCtas, "the workspace holds every CTA's partials");
-  const int c = short_cluster((int64_t)p.B * p.Hkv, max_tiles, WarpStages<E4M3>::kCtasPerSm, E4M3);
-  rtp_status st;
+  const int64_t rows = (int64_t)p.B * p.Hkv;
+  const int c = short_cluster(rows, max_tiles, per_sm, E4M3);
   if (c > 0) {
-    auto* kernel = c > 8 ? paged_attn_short_kernel<E4M3, SEL, NT, 16>
-                         : paged_attn_short_kernel<E4M3, SEL, NT, 8>;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-            cudaSuccess ||
-        (c > 8 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
-                      cudaSuccess))
-      return RTP_ERR_CUDA;
-    TraceScope tr("paged_attn", s);
-    return check_cuda(launch_dependent_cluster(kernel, dim3(p.B * p.Hkv * c), dim3(kAttnThreads), c,
-                                               smem, s, p, c));
+    // the longer of very few rows: eight warps a CTA hide more of a group's latency (4 rows
+    // of 16000 keys 11.6 us against 13.3)
+    if (c > 8)
+      return rows * c <= 64 ? launch_short<E4M3, SEL, NT, 16, 8>(p, c, s)
+                            : launch_short<E4M3, SEL, NT, 16, 4>(p, c, s);
+    return launch_short<E4M3, SEL, NT, 8, 4>(p, c, s);
   }
   auto* kernel = paged_attn_kernel<E4M3, SEL, NT>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
       cudaSuccess)
     return RTP_ERR_CUDA;
+  rtp_status st;
   {
     TraceScope tr("paged_attn", s);
     if ((st = check_cuda(launch_dependent(kernel, dim3(ctas), dim3(kAttnThreads), smem, s, p))) !=

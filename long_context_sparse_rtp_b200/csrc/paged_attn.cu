@@ -340,7 +340,7 @@ __device__ __forceinline__ void attend_run(const PagedAttnParams& p, AttnSmem<E4
     if (mask == 0u) continue;
 
     // S: 16 keys (rows) x 8 heads; this thread has keys g and g + 8
-    float s[NT][4] = {};
+    float s[NT][4] = {}, s2[NT][4] = {};  // two chains of products: half the latency
     if (E4M3) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
@@ -355,7 +355,7 @@ __device__ __forceinline__ void attend_run(const PagedAttnParams& p, AttnSmem<E4
               e4m3x2_to_f16x2((uint16_t)(x0[u] >> 16)), e4m3x2_to_f16x2((uint16_t)(x1[u] >> 16))};
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
-            mma16816_f16(s[nt], a, qb[nt][4 * j + u][0], qb[nt][4 * j + u][1]);
+            mma16816_f16(u & 1 ? s2[nt] : s[nt], a, qb[nt][4 * j + u][0], qb[nt][4 * j + u][1]);
         }
       }
     } else {
@@ -366,9 +366,13 @@ __device__ __forceinline__ void attend_run(const PagedAttnParams& p, AttnSmem<E4
         ldmatrix_x4(a, smem_u32(kt + r * kRow + (((2 * kk + (lane >> 4)) ^ (r & 7)) << 4)));
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
-          mma16816(s[nt], a, qb[nt][kk][0], qb[nt][kk][1], s[nt]);
+          mma16816(kk & 1 ? s2[nt] : s[nt], a, qb[nt][kk][0], qb[nt][kk][1], kk & 1 ? s2[nt] : s[nt]);
       }
     }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[nt][e] += s2[nt][e];
     if (mask != 0xFFFFu) {
       const bool ok0 = (mask >> g) & 1u, ok1 = (mask >> (g + 8)) & 1u;
 #pragma unroll

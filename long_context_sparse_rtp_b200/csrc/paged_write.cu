@@ -82,8 +82,8 @@ __device__ __forceinline__ uint2 quantise8(const uint4& w, const Divider& d) {
   return r;
 }
 
-constexpr int kWriteThreads = 256;
-constexpr int kWriteRows = 2;  // tokens a thread has in flight
+constexpr int kWriteThreads = 128;  // 256 threads 23.5 us where these take 21.7 (20 K tokens, 8 bits)
+constexpr int kWriteRows = 2;       // tokens a thread has in flight (1 or 4: 25 us)
 
 // A CTA takes kWriteRows times as many tokens as its threads hold rows of 16-byte
 // chunks (16 a head); a thread keeps its chunk of the row.

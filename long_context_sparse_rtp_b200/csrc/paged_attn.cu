@@ -4,22 +4,24 @@
 //   o_h = sum_j softmax_j(scale * q_h . k_j) v_j
 // over the request's keys: every key (retrieval heads), the keys of the listed
 // pages (retrieval heads with a selection), or sinks and window (local heads).
-// One pass with a running maximum and sum; requests of all lengths share the
-// GPU evenly: the tiles of 64 keys of every (request, kv head) stand in one
-// line, and each CTA takes an equal run of them.  A (request, kv head) that one
-// CTA covers is written by it; one that several cover leaves partial results
-// (m, l, o), which a second kernel joins in CTA order.
+// One pass with a running maximum and sum.  Short rows (a request's kv head is a
+// row) are split over a cluster each and joined there; otherwise requests of all
+// lengths share the GPU evenly: the tiles of 64 keys of every row stand in one
+// line, and each CTA takes an equal run of them.  A row that one CTA covers is
+// written by it; one that several cover leaves partial results (m, l, o), which a
+// second kernel joins in CTA order.
 //
-// Within a tile each of the 4 warps has a group of 16 keys, which lies in one
+// Within a tile each warp has a group of 16 keys, which lies in one
 // page, and its own ring of shared-memory stages filled by cp.async: no barrier
 // inside a run of tiles.  The tensor-core products are K Q^T (16 keys by 8 heads)
 // and V^T P^T (16 dimensions by 8 heads), P^T passing between them by an 8x8
 // transpose in registers: G <= 8 heads cost half the products, exponentials and
-// accumulators of a form with the heads as 16 rows (128K x 8, 8-bit, all heads:
-// 240 us with heads as rows, 164 so; bf16 64 ragged requests: 113 and 98).
-// Bound by HBM: 4 G flops a byte of bf16 K/V.  Three stages a warp, two CTAs an SM
-// (bf16) or three (8 bits), keep 128 and 96 KB a SM in flight; two stages and three
-// CTAs are as fast for bf16, four CTAs or six stages slower for 8 bits (167-177).
+// accumulators of a form with the heads as 16 rows (8 requests of 128K, 8-bit, all
+// heads: 240 us with heads as rows, 159 so; bf16, 64 ragged requests up to 8K: 113
+// and 94).  Bound by HBM: G flops a byte of bf16 K/V, 2 G of 8-bit.  Three stages a
+// warp, two CTAs an SM (bf16) or three (8 bits), keep 128 and 96 KB an SM in flight;
+// two stages and three CTAs are as fast for bf16, four CTAs or six stages slower for
+// 8 bits (167-177 us).
 //
 // Rounding: scores, maxima, sums and outputs in fp32; P is rounded once to the
 // 16-bit type of the P V product (bf16 beside bf16 rows; fp16 beside 8-bit ones,
@@ -194,7 +196,7 @@ __device__ __forceinline__ void attend_run(const PagedAttnParams& p, AttnSmem<E4
   const int lr_ = lane / kChunks, lc = lane % kChunks;      // this lane's row of a step and chunk
   const int64_t k_lane = lr_ * p.kp.row + lc * 16, v_lane = lr_ * p.vp.row + lc * 16;
 
-  // ---- this warp's groups: tile tt of the run is group 4 (t0 + tt) + warp
+  // ---- this warp's groups: tile tt of the run is group WARPS (t0 + tt) + warp
   const int32_t* tab = p.table + (int64_t)b * p.table_stride;
   const int32_t* sl = SEL ? p.sel + ((int64_t)b * p.n_rkv + (local ? 0 : i)) * p.n_sel : nullptr;
   // Each lane looks one tile's group up, 32 tiles at once: its physical page (-1
@@ -633,14 +635,14 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS > kAttnWarps ? 1 : WarpStage
   const cg::cluster_group cluster = cg::this_cluster();
   const int row = blockIdx.x / csize, rank = blockIdx.x % csize;
   const int b = row / p.Hkv, i = row % p.Hkv;
-  // a quarter of the warps' threads has the 128 dimensions of one query head
+  // every 128 threads have the dimensions of one query head
   constexpr int kParts = WARPS / 4;
   const int part_of = threadIdx.x >> 7, tid = threadIdx.x & 127;
   const int len = paged_len(p, b), groups = row_groups<SEL>(p, b, i, len);
   const int tiles = (groups + WARPS - 1) / WARPS;
   const int t0 = (int)((int64_t)tiles * rank / csize);
   attend_run<E4M3, SEL, NT, WARPS>(p, sm, b, i, len, groups, t0,
-                            (int)((int64_t)tiles * (rank + 1) / csize) - t0);
+                                   (int)((int64_t)tiles * (rank + 1) / csize) - t0);
 #pragma unroll 4
   for (int r = part_of; r < p.G; r += kParts) {
     float M, l, o;

@@ -10,8 +10,8 @@
 // tensor-core products give I exactly, whatever the order of summation, so the
 // selection (score descending, index ascending) is the same on every run.
 // (The integer form of those products is far slower here: 96 rows of up to 2048
-// pages took 16 us with it, traced.)  With sq * [lo8, hi8] * s_p bounding the page's keys, the score
-// bounds every q . k of the page up to the rounding of q.
+// pages took 20 us with it, 16 without, traced.)  With s_p * [lo8, hi8] bounding the
+// page's keys, the score bounds every q . k of the page up to the rounding of q.
 //
 // paged_score_kernel reads the bounds once (2 x 128 bytes and a scale a page,
 // straight into fragments: bound by HBM); paged_topn_kernel finds the n-th

@@ -12,6 +12,7 @@
 #include <ATen/cuda/EmptyTensor.h>
 #include <Python.h>
 #include <c10/cuda/CUDACachingAllocator.h>
+#include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -109,15 +110,21 @@ struct Roles {
   }
 };
 
-// Makes the call's device and stream current for as long as it lives.
+// Makes the call's device and stream current for as long as it lives.  On a stream
+// other than the caller's current one it tells the allocator who uses what: the
+// caller's tensors are in use on the call's stream, what the call allocates there is
+// used on the caller's stream too.  (Inside a capture the graph's pool holds both.)
 struct On {
   c10::cuda::OptionalCUDAGuard device;
   c10::cuda::OptionalCUDAStreamGuard guard;
+  c10::cuda::CUDAStream theirs, ours;
   cudaStream_t stream;
-  On(c10::Device dev, PyObject* s) {
+  bool crossed = false;
+  On(c10::Device dev, PyObject* s)
+      : theirs(c10::cuda::getCurrentCUDAStream(dev.index())), ours(theirs) {
     if (none(s)) {
       device.set_device(dev);
-      stream = c10::cuda::getCurrentCUDAStream(dev.index()).stream();
+      stream = ours.stream();
       return;
     }
     int64_t v[3];
@@ -131,10 +138,25 @@ struct On {
     }
     need(v[1] == dev.index() && v[2] == (int64_t)c10::DeviceType::CUDA,
          "stream: expected a stream of the tensors' device");
-    const auto st = c10::cuda::CUDAStream::unpack3(v[0], (c10::DeviceIndex)v[1],
-                                                   (c10::DeviceType)v[2]);
-    guard.reset_stream(st);
-    stream = st.stream();
+    ours = c10::cuda::CUDAStream::unpack3(v[0], (c10::DeviceIndex)v[1], (c10::DeviceType)v[2]);
+    guard.reset_stream(ours);
+    stream = ours.stream();
+    crossed = ours != theirs &&
+              c10::cuda::currentStreamCaptureStatusMayInitCtx() == c10::cuda::CaptureStatus::None;
+  }
+  void record(const at::Tensor& t, c10::cuda::CUDAStream s) const {
+    if (t.defined() && t.numel())
+      c10::cuda::CUDACachingAllocator::get()->recordStream(t.storage().data_ptr(), s);
+  }
+  // The call's arguments: tensors among them are in use on its stream.
+  void uses(PyObject* const* a, int n) const {
+    for (int i = 0; crossed && i < n; ++i)
+      if (THPVariable_Check(a[i]) && THPVariable_Unpack(a[i]).is_cuda())
+        record(THPVariable_Unpack(a[i]), ours);
+  }
+  // What the call allocated for the caller.
+  void gives(const at::Tensor& t) const {
+    if (crossed) record(t, theirs);
   }
 };
 
@@ -270,12 +292,14 @@ PyObject* plan(PyObject* const* a) {
   }
   const int64_t n_spans = std::min<int64_t>(T, T / ps + 2 * (int64_t)B);
   On on(dev, a[15]);
+  on.uses(a, 15);
   // one allocation for what the caller gave no buffer for, and the workspace
   const size_t ws_bytes = rtp_paged_workspace_size(RTP_PAGED_PLAN, B, 0, 0, nullptr, 0);
   auto padded = [](int64_t ints) { return (ints + 63) / 64 * 64; };  // 256-byte places
   const at::Tensor buf =
       empty({padded(ws_bytes / 4) + 2 * padded(B) + padded(B + 1) + padded(T) +
              padded(4 * n_spans) + padded(1)}, at::kInt, dev);
+  on.gives(buf);
   int64_t at = padded(ws_bytes / 4);
   at::Tensor out[6];
   auto take = [&](int i, const char* name, std::initializer_list<int64_t> shape,
@@ -336,6 +360,7 @@ PyObject* kv_write(PyObject* const* a) {
   const at::Tensor& slot = tensor(a[2], "slot_map", at::kInt, {T}, dev);
   const Cache c(a[3], a[4], a[5], a[6], Hkv, dev);
   On on(dev, a[7]);
+  on.uses(a, 7);
   check("rtp_paged_kv_write", rtp_paged_kv_write(T, Hkv, kr.p, kr.stride, vr.p, vr.stride, i32(slot),
                                                  c.k, c.v, c.k_scale, c.v_scale, raw(on.stream)));
   Py_RETURN_NONE;
@@ -355,6 +380,7 @@ PyObject* kv_append(PyObject* const* a) {
       tensor(a[6], "bounds", at::kChar, {c.k.n_pages, role.n_rkv, 2, kD}, dev);
   const at::Tensor& scale = tensor(a[7], "bound_scale", at::kFloat, {c.k.n_pages, role.n_rkv}, dev);
   On on(dev, a[10]);
+  on.uses(a, 10);
   check("rtp_paged_kv_append",
         rtp_paged_kv_append(T, role.Hkv, role.role, kr.p, kr.stride, vr.p, vr.stride, i32(spans),
                             count(spans.size(0), "spans: too many"), c.k, c.v, c.k_scale, c.v_scale,
@@ -380,9 +406,11 @@ PyObject* block_select(PyObject* const* a) {
   const int32_t n_sel = to_int(a[7], "n_sel");
   need(n_sel >= 1, "n_sel: expected at least 1");
   On on(dev, a[12]);
+  on.uses(a, 12);
   const int64_t n_rows = (int64_t)B * role.n_rkv;
   at::Tensor buf;  // the outputs' one allocation
   if (none(a[10]) || none(a[11])) buf = empty({n_rows * (n_sel + (int64_t)1)}, at::kInt, dev);
+  on.gives(buf);
   const at::Tensor sel = none(a[10]) ? part(buf, 0, {B, role.n_rkv, n_sel})
                                      : tensor(a[10], "sel", at::kInt, {B, role.n_rkv, n_sel}, dev);
   const at::Tensor n = none(a[11]) ? part(buf, n_rows * n_sel, {B, role.n_rkv})
@@ -425,9 +453,11 @@ PyObject* attn_decode(PyObject* const* a) {
   }
   const float scale = (float)to_double(a[12]);
   On on(dev, a[15]);
+  on.uses(a, 15);
   const int64_t o_ints = (int64_t)B * H * (kD / 2);
   at::Tensor buf;  // the outputs' one allocation
   if (none(a[13]) || none(a[14])) buf = empty({o_ints + (int64_t)B * H}, at::kInt, dev);
+  on.gives(buf);
   const at::Tensor o =
       none(a[13]) ? part(buf, 0, {B, 1, H, kD}, at::kBFloat16) : cuda_tensor(a[13], "o");
   Rows orow = {ptr(o), H * kD};

@@ -801,6 +801,41 @@ def test_calls_run_on_the_given_stream():
     assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
 
 
+def test_tensors_may_go_while_another_stream_uses_them():
+    """Inputs that the caller drops, and outputs it drops, right after a call on another
+    stream: their memory is not handed out before that stream is done with them."""
+    m = Made([500], 16, 4, (1,), seed=2)
+    want = m.attn()
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        q, table = m.q.clone(), m.table.clone()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            big = torch.zeros(1 << 28, device=DEV)
+            for _ in range(4):
+                big += 1
+        got = rtp_paged_attn_decode(q, m.k_pages, m.v_pages, table, m.seq_lens, m.roles, stream=s)
+        del q, table
+        junk = [torch.full_like(m.q, float("nan")) for _ in range(8)]
+        junk += [torch.full_like(m.table, 10 ** 6) for _ in range(8)]
+        s.synchronize()
+        assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+        # the outputs: read here behind a long queue, dropped, then s allocates again
+        torch.cuda.current_stream().wait_stream(s)
+        slow = torch.zeros(1 << 28, device=DEV)
+        for _ in range(4):
+            slow += 1
+        copy = got[0].clone()
+        del got
+        with torch.cuda.stream(s):
+            junk += [torch.full((m.q.numel() + 8,), 7.0, dtype=torch.bfloat16, device=DEV)
+                     for _ in range(8)]
+        torch.cuda.synchronize()
+        assert torch.equal(want[0], copy)
+        del junk
+
+
 # ------------------------------------------------------------------------------------- refusals
 def test_python_refusals():
     m = Made([40, 3], 16, 4, (1, 0), "e4m3", seed=1)

@@ -829,7 +829,7 @@ AttnWs attn_ws(int32_t B, int32_t Hkv, int32_t G) {
 }  // namespace
 
 size_t paged_plan_ws(int32_t B);
-size_t paged_select_ws(int32_t rows, int32_t width);
+size_t paged_select_ws(int64_t rows, int32_t width);
 
 }  // namespace rtp
 
@@ -841,7 +841,7 @@ extern "C" size_t rtp_paged_workspace_size(rtp_paged_op op, int32_t B, int32_t H
   if (op == RTP_PAGED_PLAN) return paged_plan_ws(B);
   PagedHeads ph;
   if (make_paged_heads(H, Hkv, kv_role, &ph) != RTP_OK) return kStatusBytes;
-  if (op == RTP_PAGED_SELECT) return paged_select_ws(B * ph.n_rkv, table_width);
+  if (op == RTP_PAGED_SELECT) return paged_select_ws((int64_t)B * ph.n_rkv, table_width);
   if (op == RTP_PAGED_ATTN) return attn_ws(B, Hkv, ph.G).total;
   return kStatusBytes;
 }

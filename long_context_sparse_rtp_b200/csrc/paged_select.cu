@@ -432,7 +432,7 @@ __global__ void __launch_bounds__(WARPS * 32) paged_topn_kernel(const SelectPara
 
 inline int32_t select_pitch(int32_t width) { return (width + 3) & ~3; }  // whole uint4s a row
 
-size_t paged_select_ws(int32_t rows, int32_t width) {
+size_t paged_select_ws(int64_t rows, int32_t width) {
   return align_up(kStatusBytes + (size_t)rows * select_pitch(width) * 4, 256);
 }
 
@@ -463,7 +463,7 @@ extern "C" rtp_status rtp_paged_block_select(
   if (q_stride < (int64_t)H * kD) return RTP_ERR_INVALID_ARG;
   if (!aligned16(q) || (q_stride * 2) % 16 || !aligned16(bounds) || !aligned16(ws))
     return RTP_ERR_ALIGNMENT;
-  if (ws == nullptr || ws_bytes < paged_select_ws((int32_t)rows, table_width))
+  if (ws == nullptr || ws_bytes < paged_select_ws(rows, table_width))
     return RTP_ERR_WORKSPACE_TOO_SMALL;
   SelectParams p;
   memset(&p, 0, sizeof(p));

@@ -10,8 +10,10 @@
 //   slot of position x = table[x / ps] * ps + x % ps.
 // Three running sums over the requests (tokens, pages, spans), then
 // independent writes.  What bounds it is latency: one CTA scans 1024 requests
-// at a time; with few tokens the same threads write everything (one launch),
-// with many a second kernel spreads the writes over the SMs.
+// at a time; with few tokens the same CTA writes everything (one launch), with
+// many a second kernel spreads the writes over the SMs.
+#include <algorithm>
+
 #include "paged.cuh"
 
 namespace rtp {
@@ -55,6 +57,24 @@ __device__ __forceinline__ int32_t page_of(const PlanParams& p, const int32_t* r
   return c < r.have ? row[c] : popped(p, r, c - r.have);
 }
 
+// Slot of new token t of an admitted request.
+__device__ __forceinline__ int32_t slot_of(const PlanParams& p, int b, const Req& r, int32_t t) {
+  const int32_t* row = p.table + (int64_t)b * p.table_stride;
+  const int64_t x = r.old + t;
+  const int64_t slot = ((int64_t)page_of(p, row, r, (int32_t)(x >> p.ps_shift)) << p.ps_shift) +
+                       (x & ((1 << p.ps_shift) - 1));
+  return slot >= 0 && slot <= INT32_MAX ? (int32_t)slot : -1;
+}
+
+// Span of table column c of an admitted request.
+__device__ __forceinline__ int4 span_of(const PlanParams& p, int b, const Req& r, int32_t c) {
+  const int64_t lo = (int64_t)c << p.ps_shift;
+  const int32_t rows = (int32_t)min((int64_t)1 << p.ps_shift, r.old + r.n - lo);
+  const int32_t fresh = (int32_t)max((int64_t)0, r.old - lo);
+  return make_int4(page_of(p, p.table + (int64_t)b * p.table_stride, r, c), rows, fresh,
+                   (int32_t)(r.cu + lo + fresh - r.old));
+}
+
 // Table entries, slots and spans of one request; threads i, i + step, ...  The
 // tokens of a refused one stay in the packed batch, without slots.
 __device__ __forceinline__ void fill_request(const PlanParams& p, int b, const Req& r, int i,
@@ -64,27 +84,15 @@ __device__ __forceinline__ void fill_request(const PlanParams& p, int b, const R
       min((int64_t)r.cu + (p.row_tokens > 0 ? p.row_tokens : r.n), (int64_t)p.max_tokens);
   for (int64_t t = (int64_t)r.cu + (r.ok ? r.n : 0) + i; t < slots_end; t += step) p.slot_map[t] = -1;
   if (!r.ok) return;
-  const int ps = 1 << p.ps_shift;
   int32_t* row = p.table + (int64_t)b * p.table_stride;
-  const int64_t end = r.old + r.n;
-  const int32_t want = (int32_t)((end + ps - 1) >> p.ps_shift);
+  const int32_t want = (int32_t)((r.old + r.n + (1 << p.ps_shift) - 1) >> p.ps_shift);
   for (int32_t c = r.have + i; c < want; c += step) row[c] = popped(p, r, c - r.have);
-  for (int32_t t = i; t < r.n; t += step) {
-    const int64_t x = r.old + t;
-    const int64_t slot =
-        ((int64_t)page_of(p, row, r, (int32_t)(x >> p.ps_shift)) << p.ps_shift) + (x & (ps - 1));
-    p.slot_map[r.cu + t] = slot >= 0 && slot <= INT32_MAX ? (int32_t)slot : -1;
-  }
+  for (int32_t t = i; t < r.n; t += step) p.slot_map[r.cu + t] = slot_of(p, b, r, t);
   if (r.n > 0) {
     const int32_t first = (int32_t)(r.old >> p.ps_shift);
     for (int32_t c = first + i; c < want; c += step) {
-      const int64_t lo = (int64_t)c << p.ps_shift;
-      const int32_t rows = (int32_t)min((int64_t)ps, end - lo);
-      const int32_t fresh = (int32_t)max((int64_t)0, r.old - lo);
       const int32_t at = r.span0 + c - first;
-      if (at < p.max_spans)
-        p.spans[at] = make_int4(page_of(p, row, r, c), rows, fresh,
-                                (int32_t)(r.cu + lo + fresh - r.old));
+      if (at < p.max_spans) p.spans[at] = span_of(p, b, r, c);
     }
   }
 }
@@ -96,6 +104,7 @@ __device__ __forceinline__ void pad_tail(const PlanParams& p, int64_t tokens, in
 }
 
 constexpr int kPlanThreads = 1024;
+constexpr int kPlanOneLaunch = 1024;  // tokens
 
 // Inclusive block scan; *total gets the sum over the block.
 __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* warp_sums, int64_t* total) {
@@ -119,10 +128,32 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* warp_sums, int
   return v + (warp ? before : 0);
 }
 
+// The requests of a one-launch plan, in shared memory.
+struct PlanSmem {
+  int32_t old[kPlanThreads], n[kPlanThreads], have[kPlanThreads], off[kPlanThreads];
+  int32_t cu[kPlanThreads], span0[kPlanThreads], ok[kPlanThreads];
+};
+
+// The last of the first B entries of an ascending array that is <= x (x >= at[0]).
+__device__ __forceinline__ int last_at(const int32_t* at, int B, int64_t x) {
+  int lo = 0, hi = B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (at[mid] <= x) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+// FILL (B <= threads): the same CTA then writes everything: a request's thread its one
+// or two tokens, or, where a request has more, a thread a token, a span, a page at a
+// time, whose request it finds by bisection (64 requests, one token each: 3.3 us
+// against 4.3 by bisection).
 template <bool FILL>
 __global__ void __launch_bounds__(kPlanThreads) plan_scan_kernel(const PlanParams p) {
   griddep_wait();
   __shared__ int64_t sums[32];
+  extern __shared__ __align__(16) unsigned char plan_smem[];
+  PlanSmem& sm = *reinterpret_cast<PlanSmem*>(plan_smem);
   const int tid = threadIdx.x, lane = tid & 31, n_thr = blockDim.x;
   const int ps = 1 << p.ps_shift;
   int64_t top = max(0, min(*p.free_count, p.free_cap));
@@ -152,6 +183,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_scan_kernel(const PlanParam
 
   int64_t tokens = 0, pages = 0, spans = 0;  // sums over the requests before this chunk
   int64_t taken = 0;
+  bool wide = false;
   for (int b0 = 0; b0 < p.B; b0 += n_thr) {
     const int b = b0 + tid;
     const bool live = b < p.B;
@@ -184,9 +216,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_scan_kernel(const PlanParam
     spans += all;
     block_scan(ok ? need : 0, sums, &all);
     taken += all;
-    // off only matters where need > 0, and there upto <= top fits 32 bits
+    // off only matters where pages are taken, and there it is below top
     r.have = (int32_t)min(have, (int64_t)p.width);
-    r.off = ok ? (int32_t)min(upto - need, (int64_t)INT32_MAX) : 0;
+    r.off = (int32_t)min(upto - need, (int64_t)INT32_MAX);
     r.cu = (int32_t)min(cu, (int64_t)INT32_MAX);
     r.span0 = (int32_t)min(span_end - n_span, (int64_t)INT32_MAX);
     r.ok = ok ? 1 : 0;
@@ -194,30 +226,22 @@ __global__ void __launch_bounds__(kPlanThreads) plan_scan_kernel(const PlanParam
       p.cu_new[b + 1] = (int32_t)min(cu_end, (int64_t)INT32_MAX);
       p.admitted[b] = r.ok;
       p.seq_lens_out[b] = (int32_t)(r.old + (ok ? r.n : 0));
-    }
-    if (FILL) {
-      // a token or two: the request's own thread; more: its warp, one request at a time
-      const int32_t n_slots = !live ? 0 : p.row_tokens > 0 ? p.row_tokens : r.n;
-      const bool wide = n_slots > 2;
-      if (!wide && n_slots > 0) fill_request(p, b, r, 0, 1);
-      uint32_t todo = __ballot_sync(0xffffffffu, wide);
-      while (todo) {
-        const int src = __ffs(todo) - 1;
-        todo &= todo - 1;
-        Req w;
-        w.old = __shfl_sync(0xffffffffu, r.old, src);
-        w.n = __shfl_sync(0xffffffffu, r.n, src);
-        w.have = __shfl_sync(0xffffffffu, r.have, src);
-        w.off = __shfl_sync(0xffffffffu, r.off, src);
-        w.cu = __shfl_sync(0xffffffffu, r.cu, src);
-        w.span0 = __shfl_sync(0xffffffffu, r.span0, src);
-        w.ok = __shfl_sync(0xffffffffu, r.ok, src);
-        w.top = r.top;
-        fill_request(p, b - lane + src, w, lane, 32);
+      if (FILL) {
+        sm.old[b] = (int32_t)r.old;
+        sm.n[b] = r.n;
+        sm.have[b] = r.have;
+        sm.off[b] = r.off;
+        sm.cu[b] = r.cu;
+        sm.span0[b] = r.span0;
+        sm.ok[b] = r.ok;
+        // a token or two: the request's own thread writes them
+        const int32_t slots = p.row_tokens > 0 ? p.row_tokens : r.n;
+        wide = slots > 2;
+        if (!wide && slots > 0) fill_request(p, b, r, 0, 1);
+      } else {
+        p.info[2 * b] = make_int4((int32_t)r.old, r.n, r.have, r.off);
+        p.info[2 * b + 1] = make_int4(r.cu, r.span0, r.ok, 0);
       }
-    } else if (live) {
-      p.info[2 * b] = make_int4((int32_t)r.old, r.n, r.have, r.off);
-      p.info[2 * b + 1] = make_int4(r.cu, r.span0, r.ok, 0);
     }
   }
   if (p.row_tokens > 0) tokens = (int64_t)p.B * p.row_tokens;
@@ -230,7 +254,48 @@ __global__ void __launch_bounds__(kPlanThreads) plan_scan_kernel(const PlanParam
       p.head[2] = (int32_t)min(spans, (int64_t)INT32_MAX);
     }
   }
-  if (FILL) pad_tail(p, tokens, spans, tid, n_thr);
+  if (!FILL) return;
+
+  if (!__syncthreads_or(wide)) {
+    pad_tail(p, tokens, spans, tid, n_thr);
+    return;
+  }
+  auto request = [&](int b) {
+    Req r;
+    r.old = sm.old[b];
+    r.n = sm.n[b];
+    r.have = sm.have[b];
+    r.off = sm.off[b];
+    r.cu = sm.cu[b];
+    r.span0 = sm.span0[b];
+    r.ok = sm.ok[b];
+    r.top = (int32_t)top;
+    return r;
+  };
+  for (int t = tid; t < p.max_tokens; t += n_thr) {
+    int32_t slot = -1;
+    if (t < tokens) {
+      const int b = last_at(sm.cu, p.B, t);
+      const Req r = request(b);
+      if (r.ok && t - r.cu < r.n) slot = slot_of(p, b, r, t - r.cu);
+    }
+    p.slot_map[t] = slot;
+  }
+  for (int i = tid; i < p.max_spans; i += n_thr) {
+    int4 sp = make_int4(-1, 0, 0, 0);
+    if (i < spans) {
+      const int b = last_at(sm.span0, p.B, i);
+      const Req r = request(b);
+      sp = span_of(p, b, r, (int32_t)(r.old >> p.ps_shift) + i - r.span0);
+    }
+    p.spans[i] = sp;
+  }
+  for (int64_t j = tid; j < taken; j += n_thr) {
+    const int b = last_at(sm.off, p.B, j);
+    const Req r = request(b);
+    const int32_t at = (int32_t)j - r.off;
+    p.table[(int64_t)b * p.table_stride + r.have + at] = popped(p, r, at);
+  }
 }
 
 constexpr int kFillThreads = 256;
@@ -295,11 +360,17 @@ extern "C" rtp_status rtp_paged_plan(int32_t B, int32_t page_size, int32_t row_t
                   cu_new, slot_map, reinterpret_cast<int4*>(spans), free_count_out, admitted,
                   reinterpret_cast<int4*>(w + 256), reinterpret_cast<int32_t*>(w)};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const int threads = B >= kPlanThreads ? kPlanThreads : (B + 31) / 32 * 32;
-  if (max_tokens <= 2048) {
+  // Few tokens of up to 1024 requests: one launch, with a thread for each token or
+  // request; beyond that a second kernel over all SMs.  64 requests: 300 tokens 4.4 us
+  // against 4.8 (5.5 against 7.2 from Python), 1000 tokens 6.3 against 5.0 (6.4, 7.3),
+  // 5000 tokens 9.3 against 5.0.
+  if (B <= kPlanThreads && max_tokens <= kPlanOneLaunch) {
+    const int most = std::max(B, std::min(max_tokens, kPlanThreads));
     TraceScope tr("plan_scan", s);
-    return check_cuda(launch_dependent(plan_scan_kernel<true>, dim3(1), dim3(threads), 0, s, p));
+    return check_cuda(launch_dependent(plan_scan_kernel<true>, dim3(1), dim3((most + 31) / 32 * 32),
+                                       sizeof(PlanSmem), s, p));
   }
+  const int threads = B >= kPlanThreads ? kPlanThreads : (B + 31) / 32 * 32;
   {
     TraceScope tr("plan_scan", s);
     if ((st = check_cuda(launch_dependent(plan_scan_kernel<false>, dim3(1), dim3(threads), 0, s,

@@ -37,6 +37,14 @@
 namespace rtp {
 namespace {
 
+// A row that several CTAs share, and the line's share of a CTA.
+struct SplitRow {
+  int64_t first;      // where its tiles start on the line
+  int64_t chunk;
+  int32_t row, tiles; // row -1: none
+  int32_t pad[2];
+};
+
 struct PagedAttnParams {
   const uint16_t* q; int64_t q_sb;
   uint16_t* o; int64_t o_sb;
@@ -49,7 +57,7 @@ struct PagedAttnParams {
   const int32_t* sel;             // [B][n_rkv][n_sel]
   const int32_t* sel_count;       // [B][n_rkv]
   float* part;                    // [CTAs][2][G][kPartRow]
-  int64_t* meta;                  // tiles per CTA; then each row's first tile
+  SplitRow* split;                // per CTA: the row that starts in it and goes on in the next
   float scale_log2;
   int32_t B, G, Hkv, n_rkv, H, n_pages, width, ps_shift, window, n_sink, n_sel;
   int16_t head[kMaxHeads];
@@ -87,15 +95,25 @@ __device__ __forceinline__ int row_groups(const PagedAttnParams& p, int b, int i
 }
 __device__ __forceinline__ int tiles_of(int groups) { return (groups + kAttnWarps - 1) / kAttnWarps; }
 
+// What a row takes of the line of all rows' tiles: kRowCost more than its tiles, ahead
+// of them, for starting and ending its run, so that a CTA gets fewer keys where it
+// gets many short rows (17 requests up to 5044 tokens, 5 of 8 kv heads with a window
+// of 12: 26.9 us without, 17.2 so).
+constexpr int kRowCost = 5;
+constexpr int kMinChunk = 6;  // of the line, a CTA's least share
+__device__ __forceinline__ int cost_of(int groups) {
+  return groups > 0 ? tiles_of(groups) + kRowCost : 0;
+}
+
 template <bool SEL>
-__device__ __forceinline__ int64_t request_tiles(const PagedAttnParams& p, int b) {
+__device__ __forceinline__ int64_t request_cost(const PagedAttnParams& p, int b) {
   const int len = paged_len(p, b);
   int64_t n = 0;
-  if (p.Hkv > p.n_rkv) n = (int64_t)(p.Hkv - p.n_rkv) * tiles_of(row_groups<SEL>(p, b, p.n_rkv, len));
+  if (p.Hkv > p.n_rkv) n = (int64_t)(p.Hkv - p.n_rkv) * cost_of(row_groups<SEL>(p, b, p.n_rkv, len));
   if (SEL) {
-    for (int i = 0; i < p.n_rkv; ++i) n += tiles_of(row_groups<SEL>(p, b, i, len));
+    for (int i = 0; i < p.n_rkv; ++i) n += cost_of(row_groups<SEL>(p, b, i, len));
   } else if (p.n_rkv > 0) {
-    n += (int64_t)p.n_rkv * tiles_of(row_groups<SEL>(p, b, 0, len));
+    n += (int64_t)p.n_rkv * cost_of(row_groups<SEL>(p, b, 0, len));
   }
   return n;
 }
@@ -525,7 +543,7 @@ __global__ void __launch_bounds__(kAttnThreads, WarpStages<E4M3>::kCtasPerSm)
   AttnSmem<E4M3, kAttnWarps>& sm = *reinterpret_cast<AttnSmem<E4M3, kAttnWarps>*>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  // ---- this CTA's run of tiles
+  // ---- this CTA's share of the line
   auto scan = [&](int64_t v, int64_t& all) {  // exclusive over the CTA
     int64_t x = v;
 #pragma unroll
@@ -548,7 +566,7 @@ __global__ void __launch_bounds__(kAttnThreads, WarpStages<E4M3>::kCtasPerSm)
   int64_t W = 0, mine = 0, before = 0;  // the first 128 requests' sums stay in registers
   for (int b0 = 0; b0 < p.B; b0 += kAttnThreads) {
     int64_t all;
-    const int64_t n = b0 + tid < p.B ? request_tiles<SEL>(p, b0 + tid) : 0;
+    const int64_t n = b0 + tid < p.B ? request_cost<SEL>(p, b0 + tid) : 0;
     const int64_t at = scan(n, all);
     if (b0 == 0) {
       mine = n;
@@ -556,8 +574,8 @@ __global__ void __launch_bounds__(kAttnThreads, WarpStages<E4M3>::kCtasPerSm)
     }
     W += all;
   }
-  const int64_t chunk = max((int64_t)1, (W + gridDim.x - 1) / gridDim.x);
-  if (blockIdx.x == 0 && tid == 0) p.meta[0] = chunk;
+  const int64_t chunk = max((int64_t)kMinChunk, (W + gridDim.x - 1) / gridDim.x);
+  if (tid == 0) p.split[blockIdx.x].row = -1;
   int64_t pos = (int64_t)blockIdx.x * chunk;
   const int64_t end = min(W, pos + chunk);
   if (pos >= end) return;
@@ -565,7 +583,7 @@ __global__ void __launch_bounds__(kAttnThreads, WarpStages<E4M3>::kCtasPerSm)
     const int b = (int)b0 + tid;
     int64_t n = mine, at = before, all = 0;
     if (p.B > kAttnThreads) {
-      n = b < p.B ? request_tiles<SEL>(p, b) : 0;
+      n = b < p.B ? request_cost<SEL>(p, b) : 0;
       at = run + scan(n, all);
     }
     if (at <= pos && pos < at + n) {
@@ -577,14 +595,14 @@ __global__ void __launch_bounds__(kAttnThreads, WarpStages<E4M3>::kCtasPerSm)
   __syncthreads();
   int b = sm.req, i = 0;
   int len = paged_len(p, b);
-  int64_t row0 = sm.first;  // first tile of row (b, i)
+  int64_t row0 = sm.first;  // where row (b, i) starts on the line
   const int64_t start = pos;
 
-  for (;;) {
-    // ---- the row that holds tile `pos`
+  while (pos < end) {
+    // ---- the row at `pos`
     int groups = row_groups<SEL>(p, b, i, len);
-    while (row0 + tiles_of(groups) <= pos) {
-      row0 += tiles_of(groups);
+    while (row0 + cost_of(groups) <= pos) {
+      row0 += cost_of(groups);
       if (++i == p.Hkv) {
         i = 0;
         len = paged_len(p, ++b);
@@ -592,13 +610,19 @@ __global__ void __launch_bounds__(kAttnThreads, WarpStages<E4M3>::kCtasPerSm)
       groups = row_groups<SEL>(p, b, i, len);
     }
     const int head = p.head[i];
-    const int t0 = (int)(pos - row0), tiles = tiles_of(groups);
-    const int t1 = (int)min((int64_t)tiles, t0 + (end - pos));
-    if (t0 == 0 && tid == 0) p.meta[1 + (int64_t)b * p.Hkv + i] = pos;
+    const int tiles = tiles_of(groups);
+    const int64_t tile0 = row0 + kRowCost;  // its first tile
+    const int t0 = (int)max((int64_t)0, pos - tile0);
+    const int t1 = (int)max((int64_t)0, min((int64_t)tiles, end - tile0));
+    pos = min(end, tile0 + tiles);
+    if (t1 <= t0) continue;  // only the row's own cost
+    if (t0 == 0 && t1 < tiles && tid == 0)
+      p.split[blockIdx.x] = {tile0, chunk, b * p.Hkv + i, tiles, {0, 0}};
 
     attend_run<E4M3, SEL, NT, kAttnWarps>(p, sm, b, i, len, groups, t0, t1 - t0);
     const bool whole = t0 == 0 && t1 == tiles;
-    float* part = p.part + ((int64_t)blockIdx.x * 2 + (pos == start ? 0 : 1)) * p.G * kPartRow;
+    float* part =
+        p.part + ((int64_t)blockIdx.x * 2 + (tile0 + t0 == start ? 0 : 1)) * p.G * kPartRow;
 #pragma unroll 4
     for (int r = 0; r < p.G; ++r) {
       float M, l, o;
@@ -613,8 +637,6 @@ __global__ void __launch_bounds__(kAttnThreads, WarpStages<E4M3>::kCtasPerSm)
         }
       }
     }
-    pos += t1 - t0;
-    if (pos >= end) return;
     __syncthreads();
   }
 }
@@ -684,29 +706,41 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS > kAttnWarps ? 1 : WarpStage
   cluster.sync();  // no CTA leaves while another reads its part
 }
 
-// Joins a row's partials, in CTA order, one CTA per (request, kv head, query
-// head): warp w sums a quarter of them, lane i dimensions 4 i .. 4 i + 3.  Rows
-// without keys get zeros (lse -inf); rows that one CTA covered are done already.
+// Joins the partials of the rows that several CTAs share, in CTA order.  CTA (x, r),
+// x < ctas: query head r of the row that starts in CTA x's share and goes on, if
+// there is one; each warp sums a quarter of its partials, lane i dimensions 4 i ..
+// 4 i + 3.  The CTAs behind: 128 rows each, of which those without keys get zeros
+// (lse -inf).
 template <bool SEL>
-__global__ void __launch_bounds__(128) paged_join_kernel(const PagedAttnParams p) {
+__global__ void __launch_bounds__(128) paged_join_kernel(const PagedAttnParams p, const int ctas) {
   griddep_wait();
-  const int row = blockIdx.x, r = blockIdx.y, b = row / p.Hkv, i = row % p.Hkv;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int tiles = tiles_of(row_groups<SEL>(p, b, i, paged_len(p, b)));
-  if (tiles == 0) {
-    store_final(p, b, p.head[i], r, tid, -INFINITY, 0.f, 0.f);
+  const int r = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  __shared__ float sm_m[4], sm_l[4], sm_o[4][kD];
+  if (blockIdx.x >= ctas) {
+    const int row0 = ((int)blockIdx.x - ctas) * 128, mine = row0 + tid;
+    const bool none = mine < p.B * p.Hkv &&
+                      row_groups<SEL>(p, mine / p.Hkv, mine % p.Hkv, paged_len(p, mine / p.Hkv)) == 0;
+    if (!__syncthreads_or(none)) return;
+    uint32_t* set = reinterpret_cast<uint32_t*>(sm_m);  // 128 bits
+    const uint32_t m = __ballot_sync(0xffffffffu, none);
+    if (lane == 0) set[warp] = m;
+    __syncthreads();
+    for (int k = 0; k < 128; ++k)
+      if ((set[k >> 5] >> (k & 31)) & 1u)
+        store_final(p, (row0 + k) / p.Hkv, p.head[(row0 + k) % p.Hkv], r, tid, -INFINITY, 0.f, 0.f);
     return;
   }
-  const int64_t chunk = p.meta[0], first = p.meta[1 + (int64_t)row];
-  const int64_t c0 = first / chunk, c1 = (first + tiles - 1) / chunk;
-  if (c0 == c1) return;
-  const int n = (int)(c1 - c0 + 1);
-  // the first CTA's run starts inside its share unless the row starts there
+  const SplitRow sp = p.split[blockIdx.x];
+  if (sp.row < 0) return;
+  const int b = sp.row / p.Hkv, i = sp.row % p.Hkv;
+  const int64_t c0 = blockIdx.x;
+  const int n = (int)((sp.first + sp.tiles - 1) / sp.chunk - c0 + 1);
+  // the first CTA's part is its second one unless the row's tiles start its share
   const int64_t stride = (int64_t)p.G * kPartRow;
   auto at = [&](int s) {
-    return p.part + ((c0 + s) * 2 + (s == 0 && first != c0 * chunk ? 1 : 0)) * stride + r * kPartRow;
+    return p.part + ((c0 + s) * 2 + (s == 0 && sp.first != c0 * sp.chunk ? 1 : 0)) * stride +
+           r * kPartRow;
   };
-  __shared__ float sm_m[4], sm_l[4], sm_o[4][kD];
   float M = -INFINITY;
   for (int s = tid; s < n; s += 128) M = fmaxf(M, __ldcg(at(s)));
   M = warp_max(M);
@@ -717,7 +751,7 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const PagedAttnParams p
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float l = 0.f;
   const int s0 = (int)((int64_t)n * warp / 4), s1 = (int)((int64_t)n * (warp + 1) / 4);
-#pragma unroll 4
+#pragma unroll 8
   for (int s = s0; s < s1; ++s) {
     const float* x = at(s);
     const float2 ml = __ldcg(reinterpret_cast<const float2*>(x));
@@ -741,28 +775,31 @@ constexpr int kSms = 148;
 constexpr int kMaxAttnCtas = 3 * kSms;
 
 // CTAs of a row's cluster (as many as fit on the GPU at once), 0 for the split over
-// all CTAs.  max_tiles: the longest row's, as far as the host can tell.  Up to 16
-// tiles (1024 keys) a CTA a cluster saves the second kernel and the search for the
-// run's row: 32 rows of 2000 keys 10.1 us against 12.0 (bf16), 256 rows of 500 keys
-// 15.7 against 21.5, of ragged lengths up to 1000 17.5 against 31.5.  Beyond, one long
-// request among short ones would leave most CTAs idle: with 8 of 32 rows longer than
-// the others (131072 keys against 4100) 133 us against 94.
-// Sixteen, with an SM for each CTA, suit the longer of few rows (4 rows: 4000 keys 9.6 us
-// with eight, 8.0 with sixteen; 16000 keys 13.3 against 16.0 over all CTAs), but start
-// more slowly (517 keys: 5.5 and 6.4 us).
-// A few tiles are one CTA's (100 keys: 4.0 us, a cluster 5.1).
-// Clusters need their CTAs within one of the GPU's eight groups of SMs: 128 SMs' worth
-// of clusters run at once (36 clusters of 8 at two CTAs an SM take two waves, 12.0
-// against 7.4 us).  8-bit tiles have half the bytes: there 32 a CTA, where the clusters
-// fill half the GPU or more (64 ragged rows up to 6000 keys: 18.9 against 29.8 us).
+// all CTAs.  max_tiles: the longest row's, as far as the host can tell.
+//  - Clusters need their CTAs within one of the GPU's eight groups of SMs: 128 SMs'
+//    worth of clusters run at once (36 clusters of 8 at two CTAs an SM take two waves,
+//    12.0 against 7.4 us).
+//  - Up to 16 tiles (1024 keys) a CTA a cluster saves the second kernel and the search
+//    for the run's row: 32 rows of 2000 keys 10.1 us against 12.0 (bf16).  Beyond, one
+//    long request among short ones would leave most CTAs idle: with 8 of 32 rows longer
+//    than the others (131072 keys against 4100) 133 us against 94.  8-bit tiles have
+//    half the bytes: there 32 a CTA, where the clusters fill half the GPU or more (64
+//    ragged rows up to 6000 keys: 18.9 against 29.8 us).
+//  - A few tiles are one CTA's (100 keys: 4.0 us, a cluster 5.1).
+//  - Rows that fill the GPU need no cluster: a CTA each, the next one starting where one
+//    ends, as long as the rows are not so long against their number that the last ones
+//    decide (800 rows of up to 500 keys 27.5 us against 44.2, of 4000 239 against 256,
+//    but 400 rows of 1 to 8000 keys 144 against 139).
+//  - Sixteen, with an SM for each CTA, suit the longer of few rows (4 rows: 4000 keys 8.5
+//    us, 9.0 with eight; 16000 keys 11.4, 16.0 over all CTAs), but start more slowly.
 inline int short_cluster(int64_t rows, int max_tiles, int per_sm, bool e4m3) {
   if (rows * 16 <= kSms && max_tiles > 64) return max_tiles <= 256 ? 16 : 0;
   const int slots = per_sm * 128;
   int c = max_tiles <= 4 ? 1 : 8;
   while (c > 1 && rows * c > slots) c >>= 1;
-  if (rows * c > per_sm * kSms) return 0;
+  if (c == 1 && max_tiles * (int64_t)(per_sm * kSms) <= rows * (e4m3 ? 64 : 48)) return 1;
   const int most = e4m3 && rows * c * 2 >= slots ? 32 : 16;
-  return max_tiles <= most * c ? c : 0;
+  return rows * c <= per_sm * kSms && max_tiles <= most * c ? c : 0;
 }
 
 template <bool E4M3, bool SEL, int NT, int MAXC, int WARPS>
@@ -806,8 +843,9 @@ rtp_status launch(const PagedAttnParams& p, int max_tiles, cudaStream_t s) {
       return st;
   }
   TraceScope tr("paged_join", s);
-  return check_cuda(launch_dependent(paged_join_kernel<SEL>, dim3(p.B * p.Hkv, p.G), dim3(128), 0,
-                                     s, p));
+  return check_cuda(launch_dependent(paged_join_kernel<SEL>,
+                                     dim3((unsigned)(ctas + (rows + 127) / 128), p.G), dim3(128), 0,
+                                     s, p, ctas));
 }
 
 template <bool E4M3, bool SEL>
@@ -816,12 +854,12 @@ rtp_status launch(const PagedAttnParams& p, int max_tiles, cudaStream_t s) {
 }
 
 struct AttnWs {
-  size_t meta, part, total;
+  size_t split, part, total;
 };
-AttnWs attn_ws(int32_t B, int32_t Hkv, int32_t G) {
+AttnWs attn_ws(int32_t G) {
   AttnWs w;
-  w.meta = kStatusBytes;
-  w.part = align_up(w.meta + 8 * (1 + (size_t)B * Hkv), 256);
+  w.split = kStatusBytes;
+  w.part = align_up(w.split + (size_t)kMaxAttnCtas * sizeof(SplitRow), 256);
   w.total = align_up(w.part + (size_t)kMaxAttnCtas * 2 * G * kPartRow * 4, 256);
   return w;
 }
@@ -842,7 +880,7 @@ extern "C" size_t rtp_paged_workspace_size(rtp_paged_op op, int32_t B, int32_t H
   PagedHeads ph;
   if (make_paged_heads(H, Hkv, kv_role, &ph) != RTP_OK) return kStatusBytes;
   if (op == RTP_PAGED_SELECT) return paged_select_ws((int64_t)B * ph.n_rkv, table_width);
-  if (op == RTP_PAGED_ATTN) return attn_ws(B, Hkv, ph.G).total;
+  if (op == RTP_PAGED_ATTN) return attn_ws(ph.G).total;
   return kStatusBytes;
 }
 
@@ -872,7 +910,7 @@ extern "C" rtp_status rtp_paged_attn_decode(
   if (!aligned16(q) || !aligned16(o) || (q_stride * 2) % 16 || (o_stride * 2) % 16 ||
       !aligned16(ws))
     return RTP_ERR_ALIGNMENT;
-  const AttnWs L = attn_ws(B, Hkv, ph.G);
+  const AttnWs L = attn_ws(ph.G);
   if (ws == nullptr || ws_bytes < L.total) return RTP_ERR_WORKSPACE_TOO_SMALL;
   PagedAttnParams p;
   memset(&p, 0, sizeof(p));
@@ -890,7 +928,7 @@ extern "C" rtp_status rtp_paged_attn_decode(
   p.seq_lens = seq_lens;
   p.sel = sel;
   p.sel_count = sel_count;
-  p.meta = reinterpret_cast<int64_t*>(static_cast<char*>(ws) + L.meta);
+  p.split = reinterpret_cast<SplitRow*>(static_cast<char*>(ws) + L.split);
   p.part = reinterpret_cast<float*>(static_cast<char*>(ws) + L.part);
   p.scale_log2 = softmax_scale * kLog2e;
   p.B = B;

@@ -706,17 +706,34 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS > kAttnWarps ? 1 : WarpStage
   cluster.sync();  // no CTA leaves while another reads its part
 }
 
-// Joins the partials of the rows that several CTAs share, in CTA order.  CTA (x, r),
-// x < ctas: query head r of the row that starts in CTA x's share and goes on, if
-// there is one; each warp sums a quarter of its partials, lane i dimensions 4 i ..
-// 4 i + 3.  The CTAs behind: 128 rows each, of which those without keys get zeros
-// (lse -inf).
-template <bool SEL>
-__global__ void __launch_bounds__(128) paged_join_kernel(const PagedAttnParams p, const int ctas) {
+// Joins the partials of the rows that several CTAs share, in CTA order; rows without
+// keys get zeros (lse -inf).  A CTA for query head blockIdx.y of
+//  - ROWS: row blockIdx.x, whose first CTA it looks for (few rows: as many warps as
+//    there are partials for);
+//  - else, x < ctas: the row that starts in CTA x's share and goes on, if there is
+//    one; the CTAs behind look through 128 rows each for those without keys.
+// Each warp sums an equal part of the partials, lane i dimensions 4 i .. 4 i + 3.
+template <bool SEL, bool ROWS>
+__global__ void __launch_bounds__(ROWS ? 512 : 128) paged_join_kernel(const PagedAttnParams p,
+                                                                      const int ctas) {
   griddep_wait();
+  constexpr int kThreads = ROWS ? 512 : 128, kWarps = kThreads / 32;
   const int r = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  __shared__ float sm_m[4], sm_l[4], sm_o[4][kD];
-  if (blockIdx.x >= ctas) {
+  __shared__ float sm_m[kWarps], sm_l[kWarps], sm_o[kWarps][kD];
+  __shared__ int found;
+  int64_t c0 = blockIdx.x;
+  if (ROWS) {
+    const int row = blockIdx.x, b = row / p.Hkv, i = row % p.Hkv;
+    if (tid == 0) found = -1;
+    __syncthreads();
+    for (int c = tid; c < ctas; c += kThreads)
+      if (p.split[c].row == row) found = c;
+    const bool none = row_groups<SEL>(p, b, i, paged_len(p, b)) == 0;
+    if (none && tid < kD) store_final(p, b, p.head[i], r, tid, -INFINITY, 0.f, 0.f);
+    __syncthreads();
+    c0 = found;
+    if (c0 < 0) return;  // no keys, or one CTA wrote it
+  } else if (blockIdx.x >= ctas) {
     const int row0 = ((int)blockIdx.x - ctas) * 128, mine = row0 + tid;
     const bool none = mine < p.B * p.Hkv &&
                       row_groups<SEL>(p, mine / p.Hkv, mine % p.Hkv, paged_len(p, mine / p.Hkv)) == 0;
@@ -730,10 +747,9 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const PagedAttnParams p
         store_final(p, (row0 + k) / p.Hkv, p.head[(row0 + k) % p.Hkv], r, tid, -INFINITY, 0.f, 0.f);
     return;
   }
-  const SplitRow sp = p.split[blockIdx.x];
+  const SplitRow sp = p.split[c0];
   if (sp.row < 0) return;
   const int b = sp.row / p.Hkv, i = sp.row % p.Hkv;
-  const int64_t c0 = blockIdx.x;
   const int n = (int)((sp.first + sp.tiles - 1) / sp.chunk - c0 + 1);
   // the first CTA's part is its second one unless the row's tiles start its share
   const int64_t stride = (int64_t)p.G * kPartRow;
@@ -742,15 +758,15 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const PagedAttnParams p
            r * kPartRow;
   };
   float M = -INFINITY;
-  for (int s = tid; s < n; s += 128) M = fmaxf(M, __ldcg(at(s)));
+  for (int s = tid; s < n; s += kThreads) M = fmaxf(M, __ldcg(at(s)));
   M = warp_max(M);
   if (lane == 0) sm_m[warp] = M;
   __syncthreads();
-  M = fmaxf(fmaxf(sm_m[0], sm_m[1]), fmaxf(sm_m[2], sm_m[3]));
+  M = warp_max(sm_m[lane % kWarps]);
   const float m0 = M == -INFINITY ? 0.f : M;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float l = 0.f;
-  const int s0 = (int)((int64_t)n * warp / 4), s1 = (int)((int64_t)n * (warp + 1) / 4);
+  const int s0 = (int)((int64_t)n * warp / kWarps), s1 = (int)((int64_t)n * (warp + 1) / kWarps);
 #pragma unroll 8
   for (int s = s0; s < s1; ++s) {
     const float* x = at(s);
@@ -766,8 +782,14 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const PagedAttnParams p
   reinterpret_cast<float4*>(sm_o[warp])[lane] = acc;
   if (lane == 0) sm_l[warp] = l;
   __syncthreads();
-  const float o = (sm_o[0][tid] + sm_o[1][tid]) + (sm_o[2][tid] + sm_o[3][tid]);
-  l = (sm_l[0] + sm_l[1]) + (sm_l[2] + sm_l[3]);
+  if (tid >= kD) return;
+  float o = 0.f;
+  l = 0.f;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    o += sm_o[w][tid];
+    l += sm_l[w];
+  }
   store_final(p, b, p.head[i], r, tid, M, l, o);
 }
 
@@ -843,7 +865,10 @@ rtp_status launch(const PagedAttnParams& p, int max_tiles, cudaStream_t s) {
       return st;
   }
   TraceScope tr("paged_join", s);
-  return check_cuda(launch_dependent(paged_join_kernel<SEL>,
+  if (rows <= ctas / 4)
+    return check_cuda(launch_dependent(paged_join_kernel<SEL, true>, dim3((unsigned)rows, p.G),
+                                       dim3(512), 0, s, p, ctas));
+  return check_cuda(launch_dependent(paged_join_kernel<SEL, false>,
                                      dim3((unsigned)(ctas + (rows + 127) / 128), p.G), dim3(128), 0,
                                      s, p, ctas));
 }

@@ -295,7 +295,9 @@ __global__ void __launch_bounds__(WARPS * 32) paged_topn_kernel(const SelectPara
                            [&](int i, uint32_t k) { held[i] = k; });
     __syncthreads();
   }
-  const int per = E > 0 ? E : ((nb + kThreads - 1) / kThreads + 3) & ~3;  // keys of a thread
+  // keys of a thread: whole uint4s, an odd number of them in the longer rows (at 128 bytes
+  // from thread to thread 32000 pages took 30 us, 40000 26)
+  const int per = E > 0 ? E : (((nb + kThreads - 1) / kThreads + 3) & ~3) | 4;
   const int k0 = tid * per;
   auto load4 = [&](int e, uint32_t (&k)[4]) {  // keys k0 + e ..; 0 behind the last (-inf is above)
     uint4 w = make_uint4(0u, 0u, 0u, 0u);

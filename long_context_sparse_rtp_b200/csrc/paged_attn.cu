@@ -17,8 +17,8 @@
 // and V^T P^T (16 dimensions by 8 heads), P^T passing between them by an 8x8
 // transpose in registers: G <= 8 heads cost half the products, exponentials and
 // accumulators of a form with the heads as 16 rows (8 requests of 128K, 8-bit, all
-// heads: 240 us with heads as rows, 159 so; bf16, 64 ragged requests up to 8K: 113
-// and 94).  Bound by HBM: G flops a byte of bf16 K/V, 2 G of 8-bit.  Three stages a
+// heads: 240 us with heads as rows, 164 so; bf16, 64 ragged requests up to 8K: 113
+// and 98, before the later steps).  Bound by HBM: G flops a byte of bf16 K/V, 2 G of 8-bit.  Three stages a
 // warp, two CTAs an SM (bf16) or three (8 bits), keep 128 and 96 KB an SM in flight;
 // two stages and three CTAs are as fast for bf16, four CTAs or six stages slower for
 // 8 bits (167-177 us).

@@ -209,6 +209,17 @@ def test_attn_selection_that_cannot_be_meant():
     m.check(o, lse, sel=ints([[[0, 3]], [[0, 0]]]), count=ints([[2], [0]]))
 
 
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("B,H", [(50, 4), (200, 4), (200, 32)])
+def test_attn_one_long_among_many(kv, B, H):
+    """The split over all CTAs with many rows, some of them empty, more requests than a CTA
+    scans at once, and joins of rows that many CTAs and that two CTAs share."""
+    lens = [(37 * i) % 90 for i in range(B)]
+    lens[B // 3], lens[B - 1] = 9001, 1500
+    m = Made(lens, 16, H, (1, 0), kv, seed=B)
+    m.check(*m.attn(window=70, n_sink=3), 70, 3)
+
+
 def test_attn_scale_outputs_and_strided_q():
     m = Made([100, 7], 16, 8, (1, 1), seed=6)
     big = torch.zeros(2, 1, 3, 8, D, dtype=torch.bfloat16, device=DEV)

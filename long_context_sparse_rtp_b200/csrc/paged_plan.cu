@@ -377,11 +377,11 @@ extern "C" rtp_status rtp_paged_plan(int32_t B, int32_t page_size, int32_t row_t
                                           p))) != RTP_OK)
       return st;
   }
-  // about four CTAs per SM over all requests, none with less than a step of tokens
-  int y = (int)((592 + B) / (B + 1));
-  const int most = (int)(((int64_t)max_tokens + kFillThreads - 1) / kFillThreads);
-  y = y < 1 ? 1 : (y > most ? most : y);
+  // about four CTAs per SM over all requests, none with less than a step of tokens; one
+  // at least: without tokens too the spans are padded
+  const int64_t most = ((int64_t)max_tokens + kFillThreads - 1) / kFillThreads;
+  const int y = (int)std::max<int64_t>(1, std::min((592 + (int64_t)B) / (B + (int64_t)1), most));
   TraceScope tr("plan_fill", s);
   return check_cuda(
-      launch_dependent(plan_fill_kernel, dim3(B + 1, y), dim3(kFillThreads), 0, s, p));
+      launch_dependent(plan_fill_kernel, dim3((unsigned)B + 1u, y), dim3(kFillThreads), 0, s, p));
 }

@@ -430,9 +430,9 @@ RTP_API rtp_status rtp_paged_kv_append(int32_t T, int32_t Hkv, const uint8_t* kv
  *   a_h = max_d |q_hd|, sq_h = a_h * (1/127), q8_hd = rint(q_hd / sq_h)  (fp32),
  *   I_h = sum_d max(q8_hd * bounds[0][d], q8_hd * bounds[1][d])      (whole numbers),
  *   score = max_h float(I_h) * (sq_h * bound_scale),
- * ties to the lower page; the first n_first and the last n_recent pages always
- * (n_first + n_recent <= n_sel).  A page with bound_scale = inf scores inf; a
- * head of q that is zero or not finite scores 0 everywhere.  seq_lens counts the
+ * ties to the lower page; the first n_first and the last n_recent pages always,
+ * ahead of any score (n_first + n_recent <= n_sel).  A page with bound_scale = inf
+ * scores inf; a head of q that is zero or not finite scores 0 everywhere.  seq_lens counts the
  * new token.
  * sel [B][retrieval kv heads][n_sel]: block-table columns, ascending, -1 behind
  * the last; sel_count [B][retrieval kv heads].

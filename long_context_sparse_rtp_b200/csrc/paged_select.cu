@@ -29,6 +29,9 @@ __device__ __forceinline__ float key_score(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
 }
 
+// Key of a page that is always kept: above +inf's, which any number of pages may have.
+constexpr uint32_t kForcedKey = 0xFFFFFFFFu;
+
 struct SelectParams {
   const uint16_t* q; int64_t q_sb;
   const int8_t* bounds;       // [n_pages][n_rkv][2][128]
@@ -194,8 +197,8 @@ __device__ __forceinline__ void score_pages(const SelectParams& p, ScoreSmem<NT>
       x = quad_max(x);
       const int pe = p0 + warp * 16 + s * 8 + g;
       if (t == 0 && pe < p_end) {
-        if (pe < p.n_first || pe >= nb - p.n_recent) x = INFINITY;
-        out(pe, score_key(x + 0.f));  // -0 and 0 are one score
+        const bool forced = pe < p.n_first || pe >= nb - p.n_recent;
+        out(pe, forced ? kForcedKey : score_key(x + 0.f));  // -0 and 0 are one score
       }
     }
     if (next >= p_end) return;
@@ -256,7 +259,7 @@ constexpr int kTopCand = 1024;
 // rows), reads its share again from L2 on every pass.
 //
 // The n-th largest key: 2046 equal bins over the row's finite scores, one for
-// those at +inf and one for -inf; the bin that holds it is found by a scan of the
+// those at +inf and the pages always kept, and one for -inf; the bin that holds it is found by a scan of the
 // counts, and its few keys are ranked against one another.  The bin is a
 // non-decreasing function of the score however its arithmetic rounds, so the
 // result is exact.  A bin of more than 1024 keys (mass ties) is settled bit by

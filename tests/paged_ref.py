@@ -83,7 +83,8 @@ def bounds(rows):
 
 def select(q, lo8, hi8, scale, n_sel, n_first, n_recent):
     """q [G, 128], bounds [nb, 128] and scale [nb] of a row's pages (scale < 0: no such
-    page) -> ascending page indices."""
+    page) -> ascending page indices.  The first n_first and the last n_recent pages come
+    before every other, whatever they or the others score."""
     f = np.float32
     nb = len(scale)
     if nb <= n_sel:
@@ -99,10 +100,7 @@ def select(q, lo8, hi8, scale, n_sel, n_first, n_recent):
             best = np.maximum(best, I.astype(f) * t)
     best[scale == np.inf] = np.inf
     best[scale < 0] = -np.inf
-    best[:n_first] = np.inf
-    if n_recent:
-        best[nb - n_recent:] = np.inf
-    order = sorted(range(nb), key=lambda p: (-best[p], p))
+    order = sorted(range(nb), key=lambda p: (n_first <= p < nb - n_recent, -best[p], p))
     return sorted(order[:n_sel])
 
 

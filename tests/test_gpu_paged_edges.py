@@ -3,9 +3,11 @@ that test_gpu_paged.py does not make.  Plain implementations and tolerances as t
 """
 import numpy as np
 import pytest
+import torch
 
-from long_context_sparse_rtp_b200 import rtp_paged_plan
-from test_gpu_paged import _gpu, check_plan, ints  # noqa: F401
+import paged_ref as ref
+from long_context_sparse_rtp_b200 import rtp_paged_block_select, rtp_paged_plan
+from test_gpu_paged import (D, DEV, _gpu, check_plan, check_select, ints, random_bounds, tables)  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -32,3 +34,39 @@ def test_plan_without_tokens_pads_its_spans():
     r = rtp_paged_plan(ints([3] * B), ints([0] * B), ints([[1]] * B), ints([0]), ints([0]), page_size=16,
                        max_tokens=0, out=dict(spans=spans))
     assert r["spans"].tolist() == [[-1, 0, 0, 0]] * 5
+
+
+# ------------------------------------------------------------------- pages always kept
+@pytest.mark.parametrize("width", [40, 200, 700, 4096, 17000])
+@pytest.mark.parametrize("share", [0.3, 1.0])
+def test_select_keeps_forced_pages_before_infinite_scores(width, share):
+    """More pages of scale inf than the list holds: the first and the last ones stay in it."""
+    lens = [16 * width, 16 * width - 37, 16 * 30]
+    table, n_pages = tables(lens, 16, width, seed=width)
+    b, s = random_bounds(n_pages, 2, 3)
+    g = torch.Generator(device=DEV).manual_seed(7)
+    s[torch.rand(s.shape, generator=g, device=DEV) < share] = float("inf")
+    q = torch.randn(3, 1, 4, D, generator=g, device=DEV, dtype=torch.bfloat16)
+    for n_sel, n_first, n_recent in [(1, 0, 1), (1, 1, 0), (4, 1, 1), (9, 0, 9), (20, 7, 5),
+                                     (width // 2, 3, 5)]:
+        check_select(q, b, s, table, lens, (1, 1), 16, n_sel, n_first, n_recent)
+        sel, _ = rtp_paged_block_select(q, b, s, table, ints(lens), (1, 1), page_size=16,
+                                        n_sel=n_sel, n_first=n_first, n_recent=n_recent)
+        for i, n in enumerate(lens):
+            nb = ref.up(n, 16)
+            forced = set(range(n_first)) | set(range(nb - n_recent, nb))
+            for row in sel[i].tolist():
+                assert {p for p in forced if 0 <= p < nb} <= set(row)
+
+
+def test_select_keeps_forced_pages_before_scores_that_overflow():
+    lens = [16 * 50]
+    table, n_pages = tables(lens, 16, 50, seed=3)
+    b, s = random_bounds(n_pages, 1, 4)
+    b[:, :, 1] = 127  # every page's product overflows
+    s[:] = 3e38
+    q = torch.full((1, 1, 2, D), 3e38, device=DEV, dtype=torch.bfloat16)
+    check_select(q, b, s, table, lens, (1,), 16, 3, 1, 2)
+    sel, _ = rtp_paged_block_select(q, b, s, table, ints(lens), (1,), page_size=16, n_sel=3,
+                                    n_first=1, n_recent=2)
+    assert sel.flatten().tolist() == [0, 48, 49]

@@ -316,14 +316,20 @@ __device__ __forceinline__ void attend_run(const PagedAttnParams& p, AttnSmem<E4
         a = quad_max(a);
         int ex = (int)((__float_as_uint(a) >> 23) & 0xFF) - 127;
         ex = a > 0.f ? max(-100, min(ex, 127)) : 14;
-        const float up = __uint_as_float((uint32_t)(14 - ex + 127) << 23);
+        // k_scale's sign goes into q and its size into the multiplier, which stays above zero
+        // (masked scores are -inf before it, maxima are taken before it): where it would be
+        // smaller than a normal number, scores under 2^31 times that are 0 to fp32 either way
+        const float ks = p.k_scale ? p.k_scale[head] : 1.f;
+        float up = __uint_as_float((uint32_t)(14 - ex + 127) << 23);
+        up = ks < 0.f ? -up : up;
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
 #pragma unroll
           for (int e = 0; e < 2; ++e)
             qb[nt][kk][e] = pack_f16x2(bf16_lo(qb[nt][kk][e]) * up, bf16_hi(qb[nt][kk][e]) * up);
-        const float down = p.scale_log2 * (p.k_scale ? p.k_scale[head] : 1.f) *
-                           __uint_as_float((uint32_t)(ex - 14 + 127) << 23);
+        float down = p.scale_log2 * fabsf(ks) * __uint_as_float((uint32_t)(ex - 14 + 127) << 23);
+        down = down < 0x1p-126f ? 0x1p-126f : down;
+        if (!(fabsf(ks) < INFINITY)) down = __uint_as_float(0x7FC00000u);  // NaN: so are its keys
         ms[nt][0] = __shfl_sync(0xffffffffu, down, 8 * t);
         ms[nt][1] = __shfl_sync(0xffffffffu, down, 8 * t + 4);
       }

@@ -7,7 +7,8 @@ import torch
 
 import paged_ref as ref
 from long_context_sparse_rtp_b200 import rtp_paged_block_select, rtp_paged_plan
-from test_gpu_paged import (D, DEV, _gpu, check_plan, check_select, ints, random_bounds, tables)  # noqa: F401
+from test_gpu_paged import (D, DEV, RAGGED, Made, _gpu, check_plan, check_select, ints,  # noqa: F401
+                            random_bounds, tables)
 
 pytestmark = pytest.mark.gpu
 
@@ -70,3 +71,31 @@ def test_select_keeps_forced_pages_before_scores_that_overflow():
     sel, _ = rtp_paged_block_select(q, b, s, table, ints(lens), (1,), page_size=16, n_sel=3,
                                     n_first=1, n_recent=2)
     assert sel.flatten().tolist() == [0, 48, 49]
+
+
+# ------------------------------------------------------------------- signs of 8-bit scales
+K_SCALES = [-0.02, 0.0, 0.013, -0.0, 1e-44, -1e-39, 1.2e-38, -3.0]
+
+
+@pytest.mark.parametrize("H", [8, 64, 128])
+@pytest.mark.parametrize("lens", [RAGGED, [20000, 3, 1037]])
+def test_attn_k_scales_of_any_sign(H, lens):
+    """value = scale * stored for negative, zero and tiny scales too: masked keys stay masked,
+    the running maximum is that of the scores."""
+    roles = (1, 0, 1, 1, 0, 1, 1, 1)
+    m = Made(lens, 16, H, roles, "e4m3", seed=H)
+    new = torch.tensor(K_SCALES, device=DEV)
+    m.k = [k / m.k_scale.double()[:, None] * new.double()[:, None] for k in m.k]
+    m.k_scale = new
+    m.check(*m.attn(window=37, n_sink=5), 37, 5)
+
+
+def test_attn_k_scale_not_a_number():
+    """A scale of NaN or infinity reaches its own head's outputs and no others."""
+    m = Made([40, 0, 5], 16, 4, (1, 1, 1, 1), "e4m3", seed=1)
+    m.k_scale[1], m.k_scale[2] = float("nan"), float("inf")
+    o, lse = m.attn()
+    for b in (0, 2):
+        assert bool(o[b, 0, 1:3].isnan().all()) and bool(lse[b, 1:3].isnan().all())
+        assert bool(o[b, 0, [0, 3]].isfinite().all())
+    assert bool((o[1] == 0).all()) and bool((lse[1] == float("-inf")).all())

@@ -12,7 +12,6 @@
 #include <ATen/cuda/EmptyTensor.h>
 #include <Python.h>
 #include <c10/cuda/CUDACachingAllocator.h>
-#include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -113,7 +112,8 @@ struct Roles {
 // Makes the call's device and stream current for as long as it lives.  On a stream
 // other than the caller's current one it tells the allocator who uses what: the
 // caller's tensors are in use on the call's stream, what the call allocates there is
-// used on the caller's stream too.  (Inside a capture the graph's pool holds both.)
+// used on the caller's stream too.  Inside a capture as well: a graph's pool hands what
+// was dropped out again to the stream that it was allocated on, within the capture.
 struct On {
   c10::cuda::OptionalCUDAGuard device;
   c10::cuda::OptionalCUDAStreamGuard guard;
@@ -141,8 +141,7 @@ struct On {
     ours = c10::cuda::CUDAStream::unpack3(v[0], (c10::DeviceIndex)v[1], (c10::DeviceType)v[2]);
     guard.reset_stream(ours);
     stream = ours.stream();
-    crossed = ours != theirs &&
-              c10::cuda::currentStreamCaptureStatusMayInitCtx() == c10::cuda::CaptureStatus::None;
+    crossed = ours != theirs;
   }
   void record(const at::Tensor& t, c10::cuda::CUDAStream s) const {
     if (t.defined() && t.numel())

@@ -6,7 +6,8 @@ import pytest
 import torch
 
 import paged_ref as ref
-from long_context_sparse_rtp_b200 import rtp_paged_block_select, rtp_paged_plan
+from long_context_sparse_rtp_b200 import (rtp_paged_attn_decode, rtp_paged_block_select,
+                                          rtp_paged_plan)
 from test_gpu_paged import (D, DEV, RAGGED, Made, _gpu, check_plan, check_select, ints,  # noqa: F401
                             random_bounds, tables)
 
@@ -99,3 +100,41 @@ def test_attn_k_scale_not_a_number():
         assert bool(o[b, 0, 1:3].isnan().all()) and bool(lse[b, 1:3].isnan().all())
         assert bool(o[b, 0, [0, 3]].isfinite().all())
     assert bool((o[1] == 0).all()) and bool((lse[1] == float("-inf")).all())
+
+
+# ------------------------------------------------------------------- captured, another stream
+def test_capture_on_another_stream_keeps_memory_in_use():
+    """Inside a capture too, what a call on another stream used or returned and the caller
+    dropped is not handed out again while the other stream may be using it."""
+    m = Made([700, 3], 16, 8, (1, 0), seed=5)
+    kw = dict(window=40, n_sink=2)
+    want = m.attn(**kw)
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, capture_error_mode="thread_local"):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        o, lse = m.attn(stream=side, **kw)
+        first = o.data_ptr()
+        main.wait_stream(side)
+        copy = o.clone()  # main reads it; side does not wait for that
+        del o, lse
+        o2, lse2 = m.attn(stream=side, **kw)
+        second = o2.data_ptr()
+        main.wait_stream(side)
+        q = m.q.clone()
+        used = q.data_ptr()
+        side.wait_stream(main)
+        o3, lse3 = rtp_paged_attn_decode(q, m.k_pages, m.v_pages, m.table, m.seq_lens, m.roles,
+                                         stream=side, **kw)
+        del q
+        junk = torch.full_like(m.q, float("nan"))  # main does not wait for side
+        reused = junk.data_ptr() == used
+        main.wait_stream(side)
+    assert first != second and not reused
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        for x in (copy, o2, o3):
+            assert torch.equal(x, want[0])
+        assert torch.equal(lse2, want[1]) and torch.equal(lse3, want[1])

@@ -388,8 +388,30 @@ PyObject* kv_append(PyObject* const* a) {
   Py_RETURN_NONE;
 }
 
+// (k, v, k_pages, v_pages, kv_role, k_scale, v_scale): raises what writing these rows
+// to these pages would raise, by whichever call, and does nothing.
+PyObject* check_rows(PyObject* const* a) {
+  const int32_t T = count(batch(a[0], "k", 3, "k: expected [T, Hkv, 128]"), "k: too many rows");
+  const c10::Device dev = THPVariable_Unpack(a[0]).device();
+  const Roles role(a[4]);
+  const Rows kr = rows(a[0], "k", T, role.Hkv, dev, false), vr = rows(a[1], "v", T, role.Hkv, dev, false);
+  const Cache c(a[2], a[3], a[5], a[6], role.Hkv, dev);
+  check("rtp_paged_kv_append",
+        rtp_paged_kv_append(T, role.Hkv, role.role, kr.p, kr.stride, vr.p, vr.stride, nullptr, 0, c.k,
+                            c.v, c.k_scale, c.v_scale, nullptr, nullptr, nullptr));
+  Py_RETURN_NONE;
+}
+
+// What an entry point's CHECK form hands the library: no workspace, which is the last
+// thing that a call with work to do is refused for, before anything is enqueued.
+void check_only(const char* fn, rtp_status st) {
+  check(fn, st == RTP_ERR_WORKSPACE_TOO_SMALL ? RTP_OK : st);
+}
+
 // (q, bounds, bound_scale, block_table, seq_lens, kv_role, page_size, n_sel, n_first,
 //  n_recent, sel, sel_count, stream) -> (sel, sel_count)
+// CHECK: raises what the call would raise, and does nothing.
+template <bool CHECK>
 PyObject* block_select(PyObject* const* a) {
   const int32_t B = count(batch(a[0], "q", 4, "q: expected [B, 1, H, 128]"), "q: too many requests");
   const at::Tensor& q = THPVariable_Unpack(a[0]);
@@ -404,6 +426,18 @@ PyObject* block_select(PyObject* const* a) {
   const at::Tensor& lens = tensor(a[4], "seq_lens", at::kInt, {B}, dev);
   const int32_t n_sel = to_int(a[7], "n_sel");
   need(n_sel >= 1, "n_sel: expected at least 1");
+  auto call = [&](int32_t* sel, int32_t* n, void* ws, size_t ws_bytes, rtp_stream_t stream) {
+    return rtp_paged_block_select(
+        B, H, role.Hkv, role.role, qr.p, qr.stride, static_cast<const int8_t*>(ptr(bounds)),
+        static_cast<const float*>(ptr(scale)), count(bounds.size(0), "bounds: too many pages"),
+        to_int(a[6], "page_size"), tab.p, tab.stride, tab.width, i32(lens), n_sel,
+        to_int(a[8], "n_first"), to_int(a[9], "n_recent"), sel, n, ws, ws_bytes, stream);
+  };
+  if (CHECK) {
+    int32_t none_[2];
+    check_only("rtp_paged_block_select", call(none_, none_, nullptr, 0, nullptr));
+    Py_RETURN_NONE;
+  }
   On on(dev, a[12]);
   on.uses(a, 12);
   const int64_t n_rows = (int64_t)B * role.n_rkv;
@@ -416,18 +450,15 @@ PyObject* block_select(PyObject* const* a) {
                                    : tensor(a[11], "sel_count", at::kInt, {B, role.n_rkv}, dev);
   Workspace ws(RTP_PAGED_SELECT, B, H, &role, tab.width);
   check("rtp_paged_block_select",
-        rtp_paged_block_select(B, H, role.Hkv, role.role, qr.p, qr.stride,
-                               static_cast<const int8_t*>(ptr(bounds)),
-                               static_cast<const float*>(ptr(scale)),
-                               count(bounds.size(0), "bounds: too many pages"),
-                               to_int(a[6], "page_size"), tab.p, tab.stride, tab.width, i32(lens),
-                               n_sel, to_int(a[8], "n_first"), to_int(a[9], "n_recent"), i32_out(sel),
-                               i32_out(n), ws.data.get(), ws.bytes, raw(on.stream)));
+        call(i32_out(sel), i32_out(n), ws.data.get(), ws.bytes, raw(on.stream)));
   return Py_BuildValue("NN", THPVariable_Wrap(sel), THPVariable_Wrap(n));
 }
 
 // (q, k_pages, v_pages, block_table, seq_lens, kv_role, window, n_sink, sel,
 //  sel_count, k_scale, v_scale, scale, o, lse, stream) -> (o, lse)
+// CHECK: raises what the call would raise, and does nothing; for sel the length of its
+// lists, or None, and None for sel_count.
+template <bool CHECK>
 PyObject* attn_decode(PyObject* const* a) {
   const int32_t B = count(batch(a[0], "q", 4, "q: expected [B, 1, H, 128]"), "q: too many requests");
   const at::Tensor& q = THPVariable_Unpack(a[0]);
@@ -440,36 +471,48 @@ PyObject* attn_decode(PyObject* const* a) {
   const Cache c(a[1], a[2], a[10], a[11], role.Hkv, dev);
   const Table tab(a[3], B, dev);
   const at::Tensor& lens = tensor(a[4], "seq_lens", at::kInt, {B}, dev);
-  need(none(a[8]) == none(a[9]), "sel and sel_count come together");
   const int32_t *sel = nullptr, *n = nullptr;
   int32_t n_sel = 0;
-  if (!none(a[8])) {
-    const at::Tensor& s = tensor(a[8], "sel", at::kInt, {B, role.n_rkv, kAny}, dev);
-    sel = i32(s);
-    n = i32(tensor(a[9], "sel_count", at::kInt, {B, role.n_rkv}, dev));
-    n_sel = count(s.size(2), "sel: too many pages");
-    need(role.n_rkv == 0 || n_sel >= 1, "sel: expected room for a page at least");
+  if (CHECK && !none(a[8])) {
+    sel = n = i32(lens);
+    n_sel = to_int(a[8], "n_sel");
+  } else if (!CHECK) {
+    need(none(a[8]) == none(a[9]), "sel and sel_count come together");
+    if (!none(a[8])) {
+      const at::Tensor& s = tensor(a[8], "sel", at::kInt, {B, role.n_rkv, kAny}, dev);
+      sel = i32(s);
+      n = i32(tensor(a[9], "sel_count", at::kInt, {B, role.n_rkv}, dev));
+      n_sel = count(s.size(2), "sel: too many pages");
+      need(role.n_rkv == 0 || n_sel >= 1, "sel: expected room for a page at least");
+    }
   }
   const float scale = (float)to_double(a[12]);
+  const Rows orow = none(a[13]) ? Rows{nullptr, H * kD} : rows(a[13], "o", B, H, dev, true);
+  if (!none(a[14])) tensor(a[14], "lse", at::kFloat, {B, H, 1}, dev);
+  auto call = [&](void* o, float* lse, void* ws, size_t ws_bytes, rtp_stream_t stream) {
+    return rtp_paged_attn_decode(B, H, role.Hkv, role.role, window, to_int(a[7], "n_sink"), qr.p,
+                                 qr.stride, c.k, c.v, c.k_scale, c.v_scale, tab.p, tab.stride,
+                                 tab.width, i32(lens), sel, n, n_sel, scale, o, orow.stride, lse, ws,
+                                 ws_bytes, stream);
+  };
+  if (CHECK) {
+    check_only("rtp_paged_attn_decode",
+               call(orow.p ? orow.p : qr.p, nullptr, nullptr, 0, nullptr));
+    Py_RETURN_NONE;
+  }
   On on(dev, a[15]);
   on.uses(a, 15);
   const int64_t o_ints = (int64_t)B * H * (kD / 2);
   at::Tensor buf;  // the outputs' one allocation
   if (none(a[13]) || none(a[14])) buf = empty({o_ints + (int64_t)B * H}, at::kInt, dev);
   on.gives(buf);
-  const at::Tensor o =
-      none(a[13]) ? part(buf, 0, {B, 1, H, kD}, at::kBFloat16) : cuda_tensor(a[13], "o");
-  Rows orow = {ptr(o), H * kD};
-  if (!none(a[13])) orow = rows(a[13], "o", B, H, dev, true);
+  const at::Tensor o = none(a[13]) ? part(buf, 0, {B, 1, H, kD}, at::kBFloat16)
+                                   : THPVariable_Unpack(a[13]);
   const at::Tensor lse = none(a[14]) ? part(buf, o_ints, {B, H, 1}, at::kFloat)
-                                     : tensor(a[14], "lse", at::kFloat, {B, H, 1}, dev);
+                                     : THPVariable_Unpack(a[14]);
   Workspace ws(RTP_PAGED_ATTN, B, H, &role, tab.width);
-  check("rtp_paged_attn_decode",
-        rtp_paged_attn_decode(B, H, role.Hkv, role.role, window, to_int(a[7], "n_sink"), qr.p,
-                              qr.stride, c.k, c.v, c.k_scale, c.v_scale, tab.p, tab.stride, tab.width,
-                              i32(lens), sel, n, n_sel, scale, orow.p, orow.stride,
-                              static_cast<float*>(ptr(lse)), ws.data.get(), ws.bytes,
-                              raw(on.stream)));
+  check("rtp_paged_attn_decode", call(ptr(o), static_cast<float*>(ptr(lse)), ws.data.get(),
+                                      ws.bytes, raw(on.stream)));
   return Py_BuildValue("NN", THPVariable_Wrap(o), THPVariable_Wrap(lse));
 }
 
@@ -507,8 +550,11 @@ PyMethodDef g_methods[] = {
     method<plan, 16>("plan"),
     method<kv_write, 8>("kv_write"),
     method<kv_append, 11>("kv_append"),
-    method<block_select, 13>("block_select"),
-    method<attn_decode, 16>("attn_decode"),
+    method<block_select<false>, 13>("block_select"),
+    method<attn_decode<false>, 16>("attn_decode"),
+    method<check_rows, 7>("check_rows"),
+    method<block_select<true>, 13>("check_block_select"),
+    method<attn_decode<true>, 16>("check_attn_decode"),
     {"set_error", set_error, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 

@@ -301,9 +301,10 @@ extern "C" rtp_status rtp_paged_kv_append(int32_t T, int32_t Hkv, const uint8_t*
   rtp_status st = make_paged_heads(Hkv, Hkv, kv_role, &ph);
   if (st != RTP_OK) return st;
   if ((st = check_cache(k_pages, v_pages, k_scale, v_scale)) != RTP_OK) return st;
-  if (T == 0 || n_spans == 0) return RTP_OK;
+  if (T == 0) return RTP_OK;
   if ((st = check_rows(T, Hkv, k, k_stride)) != RTP_OK) return st;
   if ((st = check_rows(T, Hkv, v, v_stride)) != RTP_OK) return st;
+  if (n_spans == 0) return RTP_OK;
   if (spans == nullptr || (ph.n_rkv > 0 && (bounds == nullptr || bound_scale == nullptr)))
     return RTP_ERR_INVALID_ARG;
   if (!aligned16(spans) || !aligned16(bounds)) return RTP_ERR_ALIGNMENT;

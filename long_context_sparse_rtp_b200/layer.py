@@ -17,8 +17,9 @@ from __future__ import annotations
 
 import torch
 
-from .paged import (rtp_paged_attn_decode, rtp_paged_block_select, rtp_paged_kv_append,
-                    rtp_paged_kv_write, rtp_paged_plan)
+from .paged import (check_attn_decode, check_block_select, check_rows, rtp_paged_attn_decode,
+                    rtp_paged_block_select, rtp_paged_kv_append, rtp_paged_kv_write,
+                    rtp_paged_plan)
 from .rtp import (rtp_index_scores, rtp_local_attn, rtp_local_attn_decode_ring,
                   rtp_local_ring_write, rtp_sparse_attn_decode, rtp_sparse_attn_decode_select,
                   rtp_sparse_attn_prefill, rtp_topp_select)
@@ -152,7 +153,10 @@ class PagedCache:
         """Takes n_new [batch] int32 new tokens per request: k, v [T, Hkv, 128], packed
         in request order, or padded to row_tokens per request.  release [batch]
         (bool or uint8): requests whose pages go back first.  Returns the plan
-        (rtp_paged_plan); plan["admitted"] says which requests were taken."""
+        (rtp_paged_plan); plan["admitted"] says which requests were taken.  A call that
+        is refused has taken nothing."""
+        check_rows(k, v, self.k_pages, self.v_pages, self.kv_role, k_scale=self.k_scale,
+                   v_scale=self.v_scale)
         plan = rtp_paged_plan(self.seq_lens, n_new, self.block_table, self.free_pages,
                               self.free_count, page_size=self.page_size, max_tokens=k.shape[0],
                               row_tokens=row_tokens, release=release,
@@ -167,15 +171,32 @@ class PagedCache:
                                 v_scale=self.v_scale, stream=stream)
         return plan
 
+    def _selects(self, n_sel):
+        if n_sel is None or not sum(self.kv_role):
+            return False
+        if self.bounds is None:
+            raise ValueError("n_sel needs a cache with bounds")
+        return True
+
+    def _check_attend(self, q, window, n_sink, n_sel, n_first, n_recent, scale, o, lse):
+        """Raises what attend would raise; enqueues nothing."""
+        if self._selects(n_sel):
+            check_block_select(q, self.bounds, self.bound_scale, self.block_table, self.seq_lens,
+                               self.kv_role, page_size=self.page_size, n_sel=n_sel,
+                               n_first=n_first, n_recent=n_recent)
+        else:
+            n_sel = None
+        check_attn_decode(q, self.k_pages, self.v_pages, self.block_table, self.seq_lens,
+                          self.kv_role, window=window, n_sink=n_sink, n_sel=n_sel,
+                          k_scale=self.k_scale, v_scale=self.v_scale, scale=scale, o=o, lse=lse)
+
     def attend(self, q, *, window=None, n_sink=0, n_sel=None, n_first=1, n_recent=1, scale=None,
                o=None, lse=None, stream=None):
         """Attention of q [batch, 1, H, 128] over the cache.  n_sel: the retrieval heads
         attend to that many pages each (rtp_paged_block_select), else to every key.
         Returns (o, lse, sel), sel = (pages, counts) or None."""
         sel = count = None
-        if n_sel is not None and sum(self.kv_role):
-            if self.bounds is None:
-                raise ValueError("n_sel needs a cache with bounds")
+        if self._selects(n_sel):
             sel, count = rtp_paged_block_select(
                 q, self.bounds, self.bound_scale, self.block_table, self.seq_lens, self.kv_role,
                 page_size=self.page_size, n_sel=n_sel, n_first=n_first, n_recent=n_recent,
@@ -196,7 +217,10 @@ def rtp_layer_decode_paged(q, k_new, v_new, cache, n_new, *, window=None, n_sink
     [B] int32: 1 for a running request, 0 for an unused row of a padded batch.
     Nothing is read on the host, so the step can be captured in a CUDA graph and
     replayed: lengths, tables and pages advance on the device.  Returns dict(o,
-    lse, sel, plan)."""
+    lse, sel, plan).  A step that is refused has taken no tokens."""
+    cache._check_attend(q, window, n_sink, n_sel, n_first, n_recent, scale, o, lse)
+    if tuple(k_new.shape[:2]) != (q.shape[0], 1) or k_new.dim() != 4 or v_new.shape != k_new.shape:
+        raise ValueError("k_new, v_new: expected [B, 1, Hkv, 128]")
     plan = cache.append(k_new.flatten(0, 1), v_new.flatten(0, 1), n_new, release=release,
                         row_tokens=1, stream=stream)
     o, lse, sel = cache.attend(q, window=window, n_sink=n_sink, n_sel=n_sel, n_first=n_first,

@@ -98,3 +98,25 @@ def rtp_paged_attn_decode(q, k_pages, v_pages, block_table, seq_lens, kv_role, *
     return (_ext or _native()).attn_decode(q, k_pages, v_pages, block_table, seq_lens, kv_role,
                                            window, n_sink, sel, sel_count, k_scale, v_scale,
                                            _SCALE if scale is None else scale, o, lse, stream)
+
+
+def check_rows(k, v, k_pages, v_pages, kv_role, *, k_scale=None, v_scale=None):
+    """Raises what rtp_paged_kv_append or rtp_paged_kv_write would raise for these rows and
+    pages; enqueues nothing."""
+    (_ext or _native()).check_rows(k, v, k_pages, v_pages, kv_role, k_scale, v_scale)
+
+
+def check_block_select(q, bounds, bound_scale, block_table, seq_lens, kv_role, *, page_size,
+                       n_sel, n_first=1, n_recent=1):
+    """Raises what rtp_paged_block_select would raise; enqueues nothing."""
+    (_ext or _native()).check_block_select(q, bounds, bound_scale, block_table, seq_lens, kv_role,
+                                           page_size, n_sel, n_first, n_recent, None, None, None)
+
+
+def check_attn_decode(q, k_pages, v_pages, block_table, seq_lens, kv_role, *, window=None, n_sink=0,
+                      n_sel=None, k_scale=None, v_scale=None, scale=None, o=None, lse=None):
+    """Raises what rtp_paged_attn_decode would raise, with lists of n_sel pages where that
+    is given; enqueues nothing."""
+    (_ext or _native()).check_attn_decode(q, k_pages, v_pages, block_table, seq_lens, kv_role,
+                                          window, n_sink, n_sel, None, k_scale, v_scale,
+                                          _SCALE if scale is None else scale, o, lse, None)

@@ -6,7 +6,8 @@ import pytest
 import torch
 
 import paged_ref as ref
-from long_context_sparse_rtp_b200 import (rtp_paged_attn_decode, rtp_paged_block_select,
+from long_context_sparse_rtp_b200 import (PagedCache, RtpError, rtp_layer_decode_paged,
+                                          rtp_paged_attn_decode, rtp_paged_block_select,
                                           rtp_paged_plan)
 from test_gpu_paged import (D, DEV, RAGGED, Made, _gpu, check_plan, check_select, ints,  # noqa: F401
                             random_bounds, tables)
@@ -138,3 +139,78 @@ def test_capture_on_another_stream_keeps_memory_in_use():
         for x in (copy, o2, o3):
             assert torch.equal(x, want[0])
         assert torch.equal(lse2, want[1]) and torch.equal(lse3, want[1])
+
+
+# ------------------------------------------------------------------- refused steps
+def state(c):
+    return [x.clone() for x in (c.seq_lens, c.free_count, c.free_pages, c.block_table)]
+
+
+def unchanged(c, was):
+    return all(torch.equal(x, y) for x, y in zip(state(c), was))
+
+
+def half_full(dtype=torch.bfloat16, **kw):
+    c = PagedCache(40, 16, (1, 0), batch=3, max_len=200, device=DEV, dtype=dtype, **kw)
+    k = torch.randn(37, 2, D, device=DEV, dtype=torch.bfloat16)
+    c.append(k, k, ints([20, 0, 17]))
+    return c, state(c)
+
+
+@pytest.mark.parametrize("bounds", [True, False])
+def test_refused_append_changes_nothing(bounds):
+    """Rows that the write would refuse are refused before the plan takes their pages."""
+    c, was = half_full(bounds=bounds)
+    k = torch.randn(5, 2, D, device=DEV, dtype=torch.bfloat16)
+    wide = torch.randn(5, 2 * D + 4, device=DEV, dtype=torch.bfloat16)
+    odd = torch.randn(5 * 2 * D + 4, device=DEV, dtype=torch.bfloat16)[4:].view(5, 2, D)
+    value = [(k, k[:4]), (k, k.float()), (k.float(), k), (k, k[:, :1]), (k[:, :1], k[:, :1]),
+             (k, k.cpu()), (k, k[:, 0]), (k, k.transpose(1, 2).contiguous().transpose(1, 2)),
+             (k, k.flip(0).transpose(0, 1)), (k[..., :64], k[..., :64])]
+    refused = [(k, wide[:, :2 * D].view(5, 2, D)), (wide[:, :2 * D].view(5, 2, D), k), (odd, k), (k, odd),
+               (k[:1].expand(5, 2, D), k)]
+    release = torch.tensor([1, 0, 1], dtype=torch.uint8, device=DEV)
+    for error, pairs in ((ValueError, value), (RtpError, refused)):
+        for x, y in pairs:
+            with pytest.raises(error):
+                c.append(x, y, ints([2, 2, 1]), release=release)
+            assert unchanged(c, was)
+    assert c.append(k, k, ints([2, 2, 1]))["admitted"].tolist() == [1, 1, 1]
+
+
+def test_refused_append_to_a_cache_with_bad_scales_changes_nothing():
+    k = torch.randn(5, 2, D, device=DEV, dtype=torch.bfloat16)
+    for dtype, scale in ((torch.bfloat16, torch.ones(2, device=DEV)), (torch.float16, None),
+                         (torch.float8_e4m3fn, torch.ones(3, device=DEV))):
+        c = PagedCache(40, 16, (1, 0), batch=3, max_len=200, device=DEV, dtype=dtype, k_scale=scale)
+        was = state(c)
+        with pytest.raises(ValueError):
+            c.append(k, k, ints([2, 2, 1]))
+        assert unchanged(c, was)
+
+
+def test_refused_step_changes_nothing():
+    """A step whose attention or selection would be refused is refused before its tokens are
+    taken."""
+    q = torch.randn(3, 1, 8, D, device=DEV, dtype=torch.bfloat16)
+    k = torch.randn(3, 1, 2, D, device=DEV, dtype=torch.bfloat16)
+    ok = dict(q=q, k=k, v=k, window=9, n_sel=4)
+    c, was = half_full()
+    for kw in (dict(q=q.float()), dict(q=q[:2]), dict(q=q[:, 0]), dict(q=q[:, :, :7]), dict(q=q.cpu()),
+               dict(k=k[:2]), dict(k=k[:, 0]), dict(v=k.float()), dict(v=k[:, :, :1]),
+               dict(k=k.expand(3, 2, 2, D), v=k.expand(3, 2, 2, D)), dict(k=k[:2], v=k[:2]),
+               dict(window=None), dict(n_sel=0), dict(o=q[:2]), dict(lse=torch.zeros(3, 8, device=DEV)),
+               dict(window=0), dict(n_sink=-1), dict(n_sel=1), dict(n_first=9), dict(n_recent=-1),
+               dict(scale=0.0), dict(scale=float("nan"))):
+        a = dict(ok, **kw)
+        args = [a.pop(x) for x in ("q", "k", "v")]
+        with pytest.raises((ValueError, RtpError)):
+            rtp_layer_decode_paged(*args, c, ints([1, 0, 1]), **a)
+        assert unchanged(c, was), kw
+    bare, was2 = half_full(bounds=False)
+    with pytest.raises(ValueError):
+        rtp_layer_decode_paged(q, k, k, bare, ints([1, 0, 1]), window=9, n_sel=4)
+    assert unchanged(bare, was2)
+    a = dict(ok)
+    r = rtp_layer_decode_paged(*[a.pop(x) for x in ("q", "k", "v")], c, ints([1, 0, 1]), **a)
+    assert r["plan"]["admitted"].tolist() == [1] * 3 and c.seq_lens.tolist() == [21, 0, 18]

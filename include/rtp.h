@@ -459,8 +459,13 @@ RTP_API rtp_status rtp_paged_block_select(
  * q, o: row of request b at q + b * q_stride elements, H heads of 128 bf16.  lse
  * (nullable): [B][H] fp32, natural log of the softmax denominator including the
  * scale.  A request without keys gets o = 0, lse = -inf; a key whose score is
- * -inf counts as absent.  The result does not depend on the other requests beyond
- * fp32 rounding (they share the split) and is the same on every run.
+ * -inf counts as absent.
+ * Scores, maxima, sums and outputs are held in fp32.  The probabilities, relative to
+ * a running reference, are rounded once for their product with V, to bf16 beside bf16
+ * pages (each off by 2^-8 of itself at most) and to fp16 beside 8-bit ones (2^-11);
+ * their sums are taken before that.  The result is the same on every run and does not
+ * depend on the other requests' values; their lengths shape the split, and with it o
+ * within that rounding and lse within fp32's.
  * Workspace: rtp_paged_workspace_size(RTP_PAGED_ATTN, ...).
  */
 RTP_API rtp_status rtp_paged_attn_decode(

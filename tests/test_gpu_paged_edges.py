@@ -214,3 +214,43 @@ def test_refused_step_changes_nothing():
     a = dict(ok)
     r = rtp_layer_decode_paged(*[a.pop(x) for x in ("q", "k", "v")], c, ints([1, 0, 1]), **a)
     assert r["plan"]["admitted"].tolist() == [1] * 3 and c.seq_lens.tolist() == [21, 0, 18]
+
+
+# ------------------------------------------------------------------- other requests
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_other_requests_change_only_the_rounding(kv):
+    """A request alone and beside others (another split, another running maximum): both within
+    the bound of P's rounding.  Other values beside it, of the same lengths: the same bits."""
+    lens = [517, 9000, 3, 517, 0, 40, 2500] + [77] * 40
+    m = Made(lens, 16, 8, (1, 0), kv, seed=21)
+    kw = dict(window=100, n_sink=3)
+    o, lse = m.attn(**kw)
+    m.check(o, lse, 100, 3)
+    u16 = 2.0 ** -11 if kv == "e4m3" else 2.0 ** -8
+    for b in (0, 1, 2, 6):
+        a, la = rtp_paged_attn_decode(m.q[b:b + 1], m.k_pages, m.v_pages, m.table[b:b + 1],
+                                      m.seq_lens[b:b + 1], m.roles, k_scale=m.k_scale,
+                                      v_scale=m.v_scale, **kw)
+        for g in range(2):
+            keys = ref.keys_of(lens[b], m.roles[g], 16, 100, 3)
+            h = slice(4 * g, 4 * g + 4)
+            eo, el, mag, sqk = ref.attend(m.q[b, 0, h], m.k[b][keys, g], m.v[b][keys, g], D ** -0.5)
+            e = (128 * 2.0 ** -24 + 2.0 ** -22) * sqk * D ** -0.5
+            nn = len(keys) * 2.0 ** -24
+            # two results, each within test_gpu_paged.py's bound of the exact value
+            tol = 2 * (2.0 ** -8 * eo.abs() + (u16 + 2 * e + 2.0 ** -20 + nn) * mag)
+            assert bool(((a[0, 0, h].double() - o[b, 0, h].double()).abs() <= tol).all())
+            lt = 2 * (e + nn + 2.0 ** -20 * (1 + float(el.abs().max())))
+            assert float((la[0, h] - lse[b, h]).abs().max()) <= lt
+    for b in (0, 6):  # the others' pages and queries change, this request's do not
+        keep = m.table[b, :ref.up(lens[b], 16)].long()
+        kp, vp, q = m.k_pages.clone(), m.v_pages.clone(), -m.q
+        mine = torch.zeros(kp.shape[0], dtype=torch.bool, device=DEV)
+        mine[keep] = True
+        for pages in (kp, vp):
+            bytes_ = pages.view(torch.uint8)
+            bytes_[~mine] = bytes_[~mine].flip(0)
+        q[b] = m.q[b]
+        o2, lse2 = rtp_paged_attn_decode(q, kp, vp, m.table, m.seq_lens, m.roles, k_scale=m.k_scale,
+                                         v_scale=m.v_scale, **kw)
+        assert torch.equal(o2[b], o[b]) and torch.equal(lse2[b], lse[b])

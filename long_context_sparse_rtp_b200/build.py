@@ -1,14 +1,20 @@
 """Build librtp.so in-tree with nvcc for sm_100a (no torch involved), and the
-Python binding of its paged calls, _paged.so, with g++ against torch.
+Python binding of its paged calls, _paged.so, with g++ against torch.  _paged.torch
+beside it names the Python and the torch it was built for; where those change it is
+built again, where they or their headers are missing it is left out with a warning
+(the paged calls then raise on first use).
 
     python -m long_context_sparse_rtp_b200.build [--force]
 """
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -17,6 +23,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "librtp.so")
 BINDING = os.path.join(CSRC, "paged_binding.cpp")
 EXT = os.path.join(HERE, "_paged.so")
+STAMP = os.path.join(HERE, "_paged.torch")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -40,13 +47,37 @@ def _stale() -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def binding_tag() -> str:
+    """What a binding depends on beside its sources: this Python and this torch."""
+    import torch
+    return (f"python {sys.version_info.major}.{sys.version_info.minor} torch {torch.__version__} "
+            f"cxx11abi {int(torch._C._GLIBCXX_USE_CXX11_ABI)}")
+
+
+def binding_built_for() -> str:
+    """The tag of the _paged.so that is there, empty without one."""
+    if not (os.path.exists(EXT) and os.path.exists(STAMP)):
+        return ""
+    with open(STAMP) as f:
+        return f.read().strip()
+
+
+def binding_needs() -> list:
+    """What is missing to build the binding."""
+    if importlib.util.find_spec("torch") is None:
+        return ["torch"]
+    from torch.utils.cpp_extension import include_paths
+    headers = {"Python.h": [sysconfig.get_paths()["include"]],
+               "torch/csrc/autograd/python_variable.h": include_paths(device_type="cuda")}
+    return [h for h, dirs in headers.items()
+            if not any(os.path.exists(os.path.join(d, h)) for d in dirs)]
+
+
 def build_binding(force: bool = False, verbose: bool = False) -> str:
     deps = [BINDING, os.path.join(INCLUDE, "rtp.h")]
-    if not force and os.path.exists(EXT) and \
+    if not force and binding_built_for() == binding_tag() and \
             all(os.path.getmtime(d) <= os.path.getmtime(EXT) for d in deps):
         return EXT
-    import sysconfig
-
     import torch
     from torch.utils.cpp_extension import include_paths, library_paths
     tmp = EXT + f".tmp{os.getpid()}"
@@ -64,12 +95,19 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
         print(" ".join(cmd))
     subprocess.check_call(cmd)
     os.replace(tmp, EXT)
+    with open(tmp, "w") as f:
+        f.write(binding_tag() + "\n")
+    os.replace(tmp, STAMP)
     return EXT
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
     build_lib(force, verbose)
-    build_binding(force, verbose)
+    missing = binding_needs()
+    if missing:
+        warnings.warn(f"the paged calls' binding is not built: no {' and no '.join(missing)}")
+    else:
+        build_binding(force, verbose)
     return LIB
 
 

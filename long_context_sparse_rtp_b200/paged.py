@@ -34,6 +34,11 @@ def _native():
             raise RuntimeError(
                 f"{EXT_PATH} is not built; run `python -m long_context_sparse_rtp_b200.build`")
         import torch  # noqa: F401  (the extension links against its libraries)
+        from . import build
+        if build.binding_built_for() not in ("", build.binding_tag()):
+            raise RuntimeError(
+                f"{EXT_PATH} was built for {build.binding_built_for()}, this is "
+                f"{build.binding_tag()}; run `python -m long_context_sparse_rtp_b200.build`")
         ext = importlib.import_module(__package__ + "._paged")
         ext.set_error(RtpError)
         _ext = ext

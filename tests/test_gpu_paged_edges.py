@@ -9,7 +9,7 @@ import paged_ref as ref
 from long_context_sparse_rtp_b200 import (PagedCache, RtpError, rtp_layer_decode_paged,
                                           rtp_paged_attn_decode, rtp_paged_block_select,
                                           rtp_paged_plan)
-from test_gpu_paged import (D, DEV, RAGGED, Made, _gpu, check_plan, check_select, ints,  # noqa: F401
+from test_gpu_paged import (D, DEV, I32, RAGGED, Made, _gpu, check_plan, check_select, ints,  # noqa: F401
                             random_bounds, tables)
 
 pytestmark = pytest.mark.gpu
@@ -254,3 +254,69 @@ def test_other_requests_change_only_the_rounding(kv):
         o2, lse2 = rtp_paged_attn_decode(q, kp, vp, m.table, m.seq_lens, m.roles, k_scale=m.k_scale,
                                          v_scale=m.v_scale, **kw)
         assert torch.equal(o2[b], o[b]) and torch.equal(lse2[b], lse[b])
+
+
+# ------------------------------------------------------------------- long loops
+@pytest.mark.parametrize("kv,n", [("bf16", 1300011), ("e4m3", 2000011)])
+@pytest.mark.parametrize("H", [8, 16])
+@pytest.mark.parametrize("listed", [False, True])
+def test_attn_runs_of_more_than_64_tiles(kv, n, H, listed):
+    """Runs long enough to look their pages up three times (32 tiles each).  Keys of zero: the
+    sums count the keys, exactly.  128 keys that one query each singles out: its value comes
+    back exactly, from the places around every look-up and elsewhere."""
+    ps, dtype = 64, torch.bfloat16 if kv == "bf16" else torch.float8_e4m3fn
+    g = torch.Generator(device=DEV).manual_seed(n % 1000 + H)
+    nb = ref.up(n, ps)
+    table = torch.randperm(nb, generator=g, device=DEV).to(I32)[None]
+    kp = torch.zeros(nb, ps, 1, D, device=DEV).to(dtype)
+    vp = torch.randint(-15, 16, (nb, ps, 1, D), generator=g, device=DEV, dtype=torch.int8).to(dtype)
+    lens = ints([n])
+    kw = {}
+    if listed:
+        kw = dict(sel=torch.arange(nb, device=DEV, dtype=I32)[None, None].contiguous(),
+                  sel_count=ints([[nb]]))
+    q = torch.zeros(1, 1, H, D, device=DEV, dtype=torch.bfloat16)
+
+    def attn():
+        return rtp_paged_attn_decode(q, kp, vp, table, lens, (1,), **kw)
+
+    o, lse = attn()
+    # P = 1 for every key: l is a whole number below 2^24 and exact, its logarithm and the
+    # product with ln 2 are each rounded; sixteen keys more or less would be 8e-6
+    assert float((lse.double() - np.log(n)).abs().max()) <= 2.0 ** -22 * (1 + np.log2(n))
+    ctas = 296 if kv == "bf16" else 444
+    chunk = ref.up(ref.up(n, 64) + 5, ctas)  # tiles a CTA takes of the line
+    assert chunk > 64
+    offs = [0, 1, 15, 16, 17, 30, 31, 32, 33, 47, 48, 49, 62, 63, 64, 65]
+    starts = torch.randint(1, ctas - 20, (7,), generator=g, device=DEV).tolist()
+    tiles = [c * chunk - 5 + x for c in starts for x in offs]
+    assert max(tiles) < n // 64
+    pos = [t * 64 + int(torch.randint(0, 64, (1,), generator=g, device=DEV)) for t in tiles]
+    pos += [0, 63, 64, n - 1, n - 12] + torch.randint(0, n, (128 - len(pos) - 5,), generator=g,
+                                                     device=DEV).tolist()
+    pos = torch.tensor(pos, device=DEV)
+    page, row = table[0].long()[pos // ps], pos % ps
+    kp[page, row, 0, torch.arange(128, device=DEV)] = torch.tensor(64.0, device=DEV).to(dtype)
+    # a score of 64 * 64 * scale = 362 against 0: the others' weights are below 2^-149
+    for d0 in range(0, 128, H):
+        q.zero_()
+        q[0, 0, torch.arange(H, device=DEV), torch.arange(d0, d0 + H, device=DEV)] = 64.0
+        o, lse = attn()
+        assert torch.equal(o[0, 0].float(), vp[page, row, 0][d0:d0 + H].float())
+
+
+@pytest.mark.parametrize("B,width,H,roles", [
+    (48, 257, 2, (1,)), (48, 512, 16, (1,)), (24, 1000, 8, (1, 1, 0, 1, 1)), (96, 1000, 1, (1,)),
+    (192, 2048, 1, (1,)), (96, 2051, 2, (1,)), (192, 3000, 1, (1,)), (3, 300, 16, (1,)),
+    (3, 5000, 32, (1, 1)), (40, 2500, 32, (1, 1)), (2, 20000, 12, (1,))])
+def test_select_many_rows_and_rounds(B, width, H, roles):
+    """Rows that fill the GPU score several rounds of pages a CTA, in one kernel and in two; more
+    than eight query heads per kv head in both."""
+    if H % len(roles):
+        H = len(roles)
+    lens = [16 * width] + [16 * (1 + (width * (37 * i % 101)) // 101) - i % 16 for i in range(1, B)]
+    table, n_pages = tables(lens, 16, width, seed=B + width)
+    b, s = random_bounds(n_pages, sum(roles), H)
+    g = torch.Generator(device=DEV).manual_seed(B)
+    q = torch.randn(B, 1, H, D, generator=g, device=DEV, dtype=torch.bfloat16)
+    check_select(q, b, s, table, lens, roles, 16, min(90, width // 2), 1, 2)

@@ -461,11 +461,12 @@ RTP_API rtp_status rtp_paged_block_select(
  * scale.  A request without keys gets o = 0, lse = -inf; a key whose score is
  * -inf counts as absent.
  * Scores, maxima, sums and outputs are held in fp32.  The probabilities, relative to
- * a running reference, are rounded once for their product with V, to bf16 beside bf16
- * pages (each off by 2^-8 of itself at most) and to fp16 beside 8-bit ones (2^-11);
- * their sums are taken before that.  The result is the same on every run and does not
- * depend on the other requests' values; their lengths shape the split, and with it o
- * within that rounding and lse within fp32's.
+ * a running reference, are rounded for their product with V: to the sum of two bf16
+ * numbers beside bf16 pages (off by 2^-15 of itself at most), to fp16 beside 8-bit
+ * ones (2^-11); their sums are taken before that.
+ * The result is the same on every run and does not depend on the other requests'
+ * values; their lengths shape the split, and with it o within that rounding and lse
+ * within fp32's.
  * Workspace: rtp_paged_workspace_size(RTP_PAGED_ATTN, ...).
  */
 RTP_API rtp_status rtp_paged_attn_decode(

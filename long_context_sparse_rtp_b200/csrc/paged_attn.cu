@@ -23,9 +23,16 @@
 // two stages and three CTAs are as fast for bf16, four CTAs or six stages slower for
 // 8 bits (167-177 us).
 //
-// Rounding: scores, maxima, sums and outputs in fp32; P is rounded once to the
-// 16-bit type of the P V product (bf16 beside bf16 rows; fp16 beside 8-bit ones,
-// whose values fp16 holds exactly), its row sums are taken before that rounding.
+// Rounding: scores, maxima, sums and outputs in fp32; row sums are taken of P before its
+// rounding to the 16-bit type of the P V product.  Beside bf16 rows that is bf16, and P
+// goes into two products: cut off to bf16, and the remainder, rounded (off by 2^-15 of P
+// at most) and not below 2^-20 P: a V of infinity takes part in both, and neither may be
+// zero there.  In one product (2^-8) the outputs were 0.0023 from 64 bits where their own
+// rounding to bf16 makes 0.0017, and the second one costs little of a
+// tensor pipe that is 9 % busy (64 requests up to 8K 89.3 -> 89.5 us, 8 x 128K mixed 92.6
+// -> 93.0).  Beside 8-bit rows it is fp16, whose values hold theirs exactly, in one
+// product: 2^-11 leaves the outputs at 0.0017, and a second product took 8 x 128K from
+// 164.5 to 171.4 us.
 // Beside 8-bit rows q is held in fp16, shifted by a power of two to a maximum in
 // [2^14, 2^15): exact but for elements under 2^-28 of the head's largest.
 #include <cooperative_groups.h>
@@ -439,7 +446,7 @@ __device__ __forceinline__ void attend_run(const PagedAttnParams& p, AttnSmem<E4
           y[nt][2 + c] = fmaf(s[nt][2 + c], ms[nt][c], to);
         }
     }
-    uint32_t pb[NT][2];
+    uint32_t pb[NT][2], pl[NT][2];  // P; beside bf16 rows the remainder of its rounding too
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       float pr[4];
@@ -447,8 +454,19 @@ __device__ __forceinline__ void attend_run(const PagedAttnParams& p, AttnSmem<E4
       for (int e = 0; e < 4; ++e) pr[e] = ex2(y[nt][e]);
       lsum[nt][0] += pr[0] + pr[2];
       lsum[nt][1] += pr[1] + pr[3];
-      pb[nt][0] = transpose8x8(E4M3 ? pack_f16x2(pr[0], pr[1]) : pack_bf16x2(pr[0], pr[1]));
-      pb[nt][1] = transpose8x8(E4M3 ? pack_f16x2(pr[2], pr[3]) : pack_bf16x2(pr[2], pr[3]));
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float p0 = pr[2 * c], p1 = pr[2 * c + 1];
+        if (E4M3) {
+          pb[nt][c] = transpose8x8(pack_f16x2(p0, p1));
+        } else {
+          const uint32_t u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
+          const float r0 = p0 - __uint_as_float(u0 & 0xFFFF0000u);
+          const float r1 = p1 - __uint_as_float(u1 & 0xFFFF0000u);
+          pb[nt][c] = transpose8x8(__byte_perm(u0, u1, 0x7632));
+          pl[nt][c] = transpose8x8(pack_bf16x2(fmaxf(r0, p0 * 0x1p-20f), fmaxf(r1, p1 * 0x1p-20f)));
+        }
+      }
     }
     if (E4M3) {
       // the thread's keys 2t, 2t+1, 2t+8, 2t+9, dimensions 16 g .. 16 g + 15:
@@ -484,8 +502,10 @@ __device__ __forceinline__ void attend_run(const PagedAttnParams& p, AttnSmem<E4
         ldmatrix_x4_trans(
             a, smem_u32(vt + r * kRow + (((2 * d + ((lane >> 3) & 1)) ^ (r & 7)) << 4)));
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
           mma16816(oacc[nt][d], a, pb[nt][0], pb[nt][1], oacc[nt][d]);
+          mma16816(oacc[nt][d], a, pl[nt][0], pl[nt][1], oacc[nt][d]);
+        }
       }
     }
   }

@@ -320,3 +320,37 @@ def test_select_many_rows_and_rounds(B, width, H, roles):
     g = torch.Generator(device=DEV).manual_seed(B)
     q = torch.randn(B, 1, H, D, generator=g, device=DEV, dtype=torch.bfloat16)
     check_select(q, b, s, table, lens, roles, 16, min(90, width // 2), 1, 2)
+
+
+# ------------------------------------------------------------------- precision
+@pytest.mark.parametrize("H,roles", [(4, (1, 1)), (32, (1, 0))])
+def test_attn_bf16_probabilities_with_their_remainder(H, roles):
+    """bf16 pages: P cut off to bf16 leaves a remainder of 2^-7 P at most, which is rounded to
+    bf16 (2^-8 of it): off by 2^-15 of P, far below what one bf16 number (2^-8) would leave in
+    outputs near zero."""
+    lens = [17, 40, 120, 300, 16 * 1700]
+    m = Made(lens, 16, H, roles, seed=H)
+    m.q *= 0.25
+    o, _ = m.attn(window=60, n_sink=3)
+    for b, n in enumerate(lens[:4]):
+        for g, role in enumerate(roles):
+            h = slice(g * m.G, (g + 1) * m.G)
+            idx = torch.tensor(ref.keys_of(n, role, 16, 60, 3), device=DEV)
+            eo, _, mag, sqk = ref.attend(m.q[b, 0, h], m.k[b][idx, g], m.v[b][idx, g], D ** -0.5)
+            e = (128 * 2.0 ** -24 + 2.0 ** -22) * sqk * D ** -0.5
+            tol = 2.0 ** -8 * eo.abs() + (2.0 ** -15 + 2 * e + 2.0 ** -20 + len(idx) * 2.0 ** -24) * mag
+            err = (o[b, 0, h].double() - eo).abs()
+            assert bool((err <= tol).all()), (b, g, float((err / tol).max()))
+
+
+def test_attn_infinite_values_beside_probabilities_that_bf16_holds():
+    """P = 1, 1 / 2, 0.3 and so on: each sign of infinity in V comes back as it is."""
+    m = Made([1, 2, 17], 16, 2, (1, 1), seed=1)
+    m.q[0], m.q[1] = 0, 0
+    for b in range(3):
+        page = int(m.table[b, 0])
+        m.v_pages[page, 0, :, 3], m.v_pages[page, 0, :, 4] = float("inf"), float("-inf")
+    o, lse = m.attn()
+    assert bool((o[..., 3] == float("inf")).all()) and bool((o[..., 4] == float("-inf")).all())
+    rest = [d for d in range(D) if d not in (3, 4)]
+    assert bool(o[..., rest].isfinite().all()) and bool(lse.isfinite().all())

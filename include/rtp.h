@@ -332,7 +332,10 @@ RTP_API rtp_status rtp_dense_attn(const rtp_shape* shape, rtp_view q, rtp_view k
  * so a step can be captured once in a CUDA graph and replayed while the
  * requests grow.  Entries that cannot be meant (a negative length, a length
  * beyond the table, a page outside the pool) are never followed: such keys count
- * as absent, such rows are not written.  A table covers at most 2^30 positions.
+ * as absent, such rows are not written.  A table, and a list of selected pages,
+ * covers at most 2^30 positions, a pool 2^31 - 1; larger ones are refused.  The
+ * kernels are chosen by the table's width (the lengths are on the device), so a table
+ * much wider than its requests need costs short ones some time.
  * The workspaces of these calls need no initialisation and carry nothing from
  * one call to the next; concurrent calls must not share one.
  */
@@ -438,7 +441,7 @@ RTP_API rtp_status rtp_paged_kv_append(int32_t T, int32_t Hkv, const uint8_t* kv
  * Stored values are ranked: beside a positive k_scale the order is that of the keys'
  * values too, beside a negative one it is not.
  * sel [B][retrieval kv heads][n_sel]: block-table columns, ascending, -1 behind
- * the last; sel_count [B][retrieval kv heads].
+ * the last; sel_count [B][retrieval kv heads].  At most 65535 such rows a call.
  * Workspace: rtp_paged_workspace_size(RTP_PAGED_SELECT, ...).
  */
 RTP_API rtp_status rtp_paged_block_select(

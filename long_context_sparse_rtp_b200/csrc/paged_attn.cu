@@ -18,21 +18,20 @@
 // transpose in registers: G <= 8 heads cost half the products, exponentials and
 // accumulators of a form with the heads as 16 rows (8 requests of 128K, 8-bit, all
 // heads: 240 us with heads as rows, 164 so; bf16, 64 ragged requests up to 8K: 113
-// and 98, before the later steps).  Bound by HBM: G flops a byte of bf16 K/V, 2 G of 8-bit.  Three stages a
-// warp, two CTAs an SM (bf16) or three (8 bits), keep 128 and 96 KB an SM in flight;
-// two stages and three CTAs are as fast for bf16, four CTAs or six stages slower for
-// 8 bits (167-177 us).
+// and 98, before the later steps).  Bound by HBM: G flops a byte of bf16 K/V, 2 G of
+// 8-bit.  Three stages a warp, two CTAs an SM (bf16) or three (8 bits), keep 128 and 96 KB
+// an SM in flight; two stages and three CTAs are as fast for bf16, four CTAs or six stages
+// slower for 8 bits (167-177 us).
 //
 // Rounding: scores, maxima, sums and outputs in fp32; row sums are taken of P before its
 // rounding to the 16-bit type of the P V product.  Beside bf16 rows that is bf16, and P
 // goes into two products: cut off to bf16, and the remainder, rounded (off by 2^-15 of P
 // at most) and not below 2^-20 P: a V of infinity takes part in both, and neither may be
 // zero there.  In one product (2^-8) the outputs were 0.0023 from 64 bits where their own
-// rounding to bf16 makes 0.0017, and the second one costs little of a
-// tensor pipe that is 9 % busy (64 requests up to 8K 89.3 -> 89.5 us, 8 x 128K mixed 92.6
-// -> 93.0).  Beside 8-bit rows it is fp16, whose values hold theirs exactly, in one
-// product: 2^-11 leaves the outputs at 0.0017, and a second product took 8 x 128K from
-// 164.5 to 171.4 us.
+// rounding to bf16 makes 0.0017; the second one takes the tensor pipe from 9 to 14 % (64
+// requests up to 8K 89.3 -> 89.5 us, 8 x 128K mixed 92.6 -> 93.0).  Beside 8-bit rows it
+// is fp16, whose values hold theirs exactly, in one product: 2^-11 leaves the outputs at
+// 0.0017, and a second product took 8 x 128K from 164.5 to 171.4 us.
 // Beside 8-bit rows q is held in fp16, shifted by a power of two to a maximum in
 // [2^14, 2^15): exact but for elements under 2^-28 of the head's largest.
 #include <cooperative_groups.h>
@@ -823,7 +822,10 @@ constexpr int kSms = 148;
 constexpr int kMaxAttnCtas = 3 * kSms;
 
 // CTAs of a row's cluster (as many as fit on the GPU at once), 0 for the split over
-// all CTAs.  max_tiles: the longest row's, as far as the host can tell.
+// all CTAs.  max_tiles: the longest row's, as far as the host can tell, which is what the
+// block table can hold; the times below are of tables as wide as their longest request
+// (one request of 517 tokens 5.5 us, in a table of 2048 pages of 16, which is split over
+// all CTAs, 9.8; 24 requests up to 2000 15.9 in either).
 //  - Clusters need their CTAs within one of the GPU's eight groups of SMs: 128 SMs'
 //    worth of clusters run at once (36 clusters of 8 at two CTAs an SM take two waves,
 //    12.0 against 7.4 us).

@@ -130,7 +130,8 @@ class PagedCache:
     tokens each: the pages, the block table, the lengths and the free pages, all
     on the GPU.  dtype torch.bfloat16, or torch.float8_e4m3fn with fp32 scales per
     kv head (k_scale, v_scale [Hkv]).  bounds=True keeps the page bounds that
-    rtp_paged_block_select reads."""
+    rtp_paged_block_select reads.  The attention and the selection choose their kernels
+    by max_len: one far above the lengths met costs short requests some time."""
 
     def __init__(self, n_pages, page_size, kv_role, *, batch, max_len, device,
                  dtype=torch.bfloat16, k_scale=None, v_scale=None, bounds=True):

@@ -466,7 +466,8 @@ RTP_API rtp_status rtp_paged_block_select(
  * Scores, maxima, sums and outputs are held in fp32.  The probabilities, relative to
  * a running reference, are rounded for their product with V: to the sum of two bf16
  * numbers beside bf16 pages (off by 2^-15 of itself at most), to fp16 beside 8-bit
- * ones (2^-11); their sums are taken before that.
+ * ones (by 2^-11 of itself, or by 2^-33 of the largest); their sums are taken before
+ * that.
  * The result is the same on every run and does not depend on the other requests'
  * values; their lengths shape the split, and with it o within that rounding and lse
  * within fp32's.

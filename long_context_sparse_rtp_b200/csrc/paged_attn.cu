@@ -30,8 +30,9 @@
 // zero there.  In one product (2^-8) the outputs were 0.0023 from 64 bits where their own
 // rounding to bf16 makes 0.0017; the second one takes the tensor pipe from 9 to 14 % (64
 // requests up to 8K 89.3 -> 89.5 us, 8 x 128K mixed 92.6 -> 93.0).  Beside 8-bit rows it
-// is fp16, whose values hold theirs exactly, in one product: 2^-11 leaves the outputs at
-// 0.0017, and a second product took 8 x 128K from 164.5 to 171.4 us.
+// is fp16, whose values hold theirs exactly, in one product: 2^-11 (2^-33 of the largest
+// P, where it is subnormal) leaves the outputs at 0.0017, and a second product took 8 x
+// 128K from 164.5 to 171.4 us.
 // Beside 8-bit rows q is held in fp16, shifted by a power of two to a maximum in
 // [2^14, 2^15): exact but for elements under 2^-28 of the head's largest.
 #include <cooperative_groups.h>

@@ -354,3 +354,25 @@ def test_attn_infinite_values_beside_probabilities_that_bf16_holds():
     assert bool((o[..., 3] == float("inf")).all()) and bool((o[..., 4] == float("-inf")).all())
     rest = [d for d in range(D) if d not in (3, 4)]
     assert bool(o[..., rest].isfinite().all()) and bool(lse.isfinite().all())
+
+
+def test_attn_small_probabilities_beside_8_bit_pages():
+    """Peaked rows: P below 2^-22 of the largest is subnormal in fp16, off by 2^-33 of the
+    largest at most, which outputs next to zero show (a V of zero beside the largest P)."""
+    m = Made([60, 300, 5], 16, 16, (1, 1, 1, 1), "e4m3", seed=5)
+    m.q *= 20
+    page = m.v_pages.view(torch.uint8)
+    for b in range(3):
+        for g in range(4):
+            best = int((m.q[b, 0, 4 * g].double() @ m.k[b][:, g].T).argmax())
+            page[int(m.table[b, best // 16]), best % 16, g] = 0
+            m.v[b][best, g] = 0
+    o, _ = m.attn()
+    for b, n in enumerate(m.lens):
+        for g in range(4):
+            h = slice(4 * g, 4 * g + 4)
+            eo, _, mag, sqk = ref.attend(m.q[b, 0, h], m.k[b][:, g], m.v[b][:, g], D ** -0.5)
+            e = (128 * 2.0 ** -24 + 2.0 ** -22) * sqk * D ** -0.5
+            tol = 2.0 ** -8 * eo.abs() + (2.0 ** -11 + 2 * e + 2.0 ** -20 + n * 2.0 ** -24) * mag + \
+                n * 2.0 ** -33 * float(m.v[b][:, g].abs().max())
+            assert bool(((o[b, 0, h].double() - eo).abs() <= tol).all()), (b, g)

@@ -325,8 +325,8 @@ RTP_API rtp_status rtp_dense_attn(const rtp_shape* shape, rtp_view q, rtp_view k
  * K and V pages are bf16, or e4m3 with one fp32 scale per kv head (value =
  * scale * stored, whatever its sign; a null scale array means 1; keys beside a scale
  * that is not finite are NaN), in any order of rows and heads: strides are in
- * elements, all multiples of 16 bytes.  Head dimension 128, at
- * most 16 query heads per kv head, kv_role as everywhere (1 = retrieval).
+ * elements, all multiples of 16 bytes.  Head dimension 128, at most 16 query heads per
+ * kv head, kv_role as everywhere (1 = retrieval).
  *
  * Lengths, tables and lists are DEVICE arrays: no call needs them on the host,
  * so a step can be captured once in a CUDA graph and replayed while the
@@ -436,8 +436,8 @@ RTP_API rtp_status rtp_paged_kv_append(int32_t T, int32_t Hkv, const uint8_t* kv
  *   score = max_h float(I_h) * (sq_h * bound_scale),
  * ties to the lower page; the first n_first and the last n_recent pages always,
  * ahead of any score (n_first + n_recent <= n_sel).  A page with bound_scale = inf
- * scores inf; a head of q that is zero or not finite scores 0 everywhere.  seq_lens counts the
- * new token.
+ * scores inf; a head of q that is zero or not finite scores 0 everywhere.  seq_lens
+ * counts the new token.
  * Stored values are ranked: beside a positive k_scale the order is that of the keys'
  * values too, beside a negative one it is not.
  * sel [B][retrieval kv heads][n_sel]: block-table columns, ascending, -1 behind
